@@ -385,6 +385,154 @@ typedef struct {
 size_t ssm_ssd_workspace_size(const ssm_ssd_args *args);  /* 0 for invalid shapes */
 ssm_status ssm_ssd_fwd(const ssm_ssd_args *args, void *stream);
 
+/*
+ * The gated linear recurrence: one real state per channel, its decay and its input gated
+ * by the token (the summary's Theorem 1 reads the S6 layer with one state as such a gated
+ * recurrence; this form gives the decay a learned rate per channel and scales the input
+ * so that the state keeps its variance). Per sequence b and channel d:
+ *   w_t    = c softplus(lam[d]) sigmoid(r_t)
+ *   a_t    = exp(-w_t),  beta_t = sqrt(1 - a_t^2)
+ *   h_t    = a_t h_{t-1} + beta_t sigmoid(i_t) x_t,   y_t = h_t
+ * and, where reset[b, t] is not 0 (a new document begins), a_t = 0 and beta_t = 1: the
+ * state before it is dropped, whatever it holds. The state and every factor are float32
+ * (1 - a_t is formed without cancellation); y is rounded once. Neighbouring pieces of
+ * time are combined in an order that depends on the shape alone, so results repeat bit
+ * for bit.
+ *
+ * x, r, i may be strided: element [b, t, d] of x lies at x + b x_stride[0] + t x_stride[1]
+ * + d (strides in elements, not negative), so that slices of one projection are read in
+ * place. All other arrays are contiguous. Any dim and seqlen; tokens on their element
+ * size, float arrays on 4 bytes. Where dim and the strides are even and the token arrays
+ * start on two elements (float arrays on 8 bytes), a lane takes two channels.
+ *
+ * states (optional output) receives what the backward needs of the forward: the state
+ * before every SSM_GATED_CHUNK-th step, [B, ceil(L / SSM_GATED_CHUNK), D] float32
+ * (ssm_gated_states_size() bytes). y may be NULL when states or h_last is wanted only.
+ * L == 0 writes h_last = h0 (or 0). Outputs must not alias inputs.
+ * Errors: SSM_ERR_INVALID for sizes or strides below zero, c not positive and finite,
+ * missing pointers, unknown dtype or flags, a short workspace; SSM_ERR_UNSUPPORTED for
+ * misaligned pointers and sizes beyond 2^56 elements or 2^31 tiles.
+ */
+#define SSM_GATED_CHUNK 64
+
+typedef struct {
+    int64_t batch, seqlen, dim;
+    ssm_dtype dtype;         /* of x, r, i, y                                         */
+    uint32_t flags;          /* 0                                                     */
+    float c;                 /* scale of the rate (8 is usual)                        */
+    const void *x;           /* [B, L, D] input                                       */
+    const void *r;           /* [B, L, D] decay gate, before its sigmoid              */
+    const void *i;           /* [B, L, D] input gate, before its sigmoid              */
+    int64_t x_stride[2], r_stride[2], i_stride[2]; /* elements between sequences, between steps */
+    const uint8_t *reset;    /* [B, L] or NULL                                        */
+    const float *lam;        /* [D] rate parameter                                    */
+    const float *h0;         /* [B, D] initial state or NULL for 0                    */
+    void *y;                 /* [B, L, D] output, dtype of x, or NULL                 */
+    float *h_last;           /* [B, D] final state out or NULL                        */
+    float *states;           /* [B, ceil(L / SSM_GATED_CHUNK), D] out or NULL         */
+    void *workspace;         /* ssm_gated_scan_workspace_size() bytes, on 16          */
+    size_t workspace_bytes;
+} ssm_gated_args;
+
+size_t ssm_gated_states_size(int64_t batch, int64_t seqlen, int64_t dim);
+size_t ssm_gated_scan_workspace_size(const ssm_gated_args *args); /* 0 for invalid arguments */
+ssm_status ssm_gated_scan_fwd(const ssm_gated_args *args, void *stream);
+
+/*
+ * Backward of ssm_gated_scan_fwd, given dy = dL/dy and optionally dh_last = dL/dh_L. With
+ * v_t = dL/dh_t = dy_t + a_{t+1} v_{t+1} (v_{L-1} also takes dh_last) and u_t = sigmoid(i_t) x_t:
+ *   dw_t = a_t v_t (a_t u_t / beta_t - h_{t-1})      (0 at a reset)
+ *   dr_t = dw_t w_t (1 - sigmoid(r_t))
+ *   dlam = c sigmoid(lam) sum_{b,t} dw_t sigmoid(r_t)
+ *   dx_t = v_t beta_t sigmoid(i_t),   di_t = v_t beta_t u_t (1 - sigmoid(i_t)),   dh0 = a_0 v_0
+ * The states before every chunk come from the forward (states); the others are computed
+ * again from them. dx, dr, di [B, L, D] contiguous, dtype of x; dlam [D], dh0 [B, D] (or
+ * NULL) float32. Every sum has a fixed order: results repeat bit for bit. Where a_t rounds
+ * to 1 (beta_t = 0) dr_t and the step's part of dlam are 0. Errors as for the forward.
+ */
+typedef struct {
+    int64_t batch, seqlen, dim;
+    ssm_dtype dtype;
+    uint32_t flags;          /* 0                                                     */
+    float c;
+    const void *x, *r, *i;   /* the forward's inputs                                  */
+    int64_t x_stride[2], r_stride[2], i_stride[2];
+    const uint8_t *reset;
+    const float *lam;
+    const float *states;     /* the forward's states                                  */
+    const void *dy;          /* [B, L, D] dtype of x                                  */
+    const float *dh_last;    /* [B, D] or NULL for 0                                  */
+    void *dx, *dr, *di;      /* [B, L, D] outputs                                     */
+    float *dlam;             /* [D] output                                            */
+    float *dh0;              /* [B, D] output or NULL                                 */
+    void *workspace;         /* ssm_gated_scan_bwd_workspace_size() bytes, on 16      */
+    size_t workspace_bytes;
+} ssm_gated_bwd_args;
+
+size_t ssm_gated_scan_bwd_workspace_size(const ssm_gated_bwd_args *args);
+ssm_status ssm_gated_scan_bwd(const ssm_gated_bwd_args *args, void *stream);
+
+/*
+ * One token of the gated recurrence for every sequence and channel: x, r, i [B, D] with a
+ * stride in elements between sequences, lam [D], h [B, D] float32 read, h_out [B, D]
+ * written (h itself, or memory that does not overlap it), y [B, D]. No workspace. Errors
+ * as for ssm_gated_scan_fwd.
+ */
+ssm_status ssm_gated_step(int64_t batch, int64_t dim, ssm_dtype dtype, float c, const void *x, int64_t x_stride,
+                          const void *r, int64_t r_stride, const void *i, int64_t i_stride, const float *lam,
+                          const float *h, float *h_out, void *y, void *stream);
+
+/*
+ * Layer norm of the rows of s = x + residual (or of x alone), the norm in front of a
+ * residual block's mixer:
+ *   y = (s - mean(s)) rstd weight + bias,  rstd = 1 / sqrt(var(s) + eps)
+ * x, y [rows, dim] of dtype; residual and residual_out (= s) [rows, dim] float32, both or
+ * neither (the residual stream is kept in float32; residual_out may be residual itself);
+ * weight [dim], bias [dim] (or NULL) float32; mean, rstd [rows] float32 out, or NULL.
+ * Contiguous arrays; 1 <= dim <= 16384, rows < 2^31 (SSM_ERR_UNSUPPORTED beyond; no rows
+ * or no columns: nothing to do). Sums, mean and rstd are float32, the variance a second
+ * pass over the centred row. Arrays on 16 bytes and dim a multiple of 8 (bfloat16) or 4
+ * (float32) are moved 16 bytes at a time, others element by element. eps >= 0.
+ */
+typedef struct {
+    int64_t rows, dim;
+    ssm_dtype dtype;         /* of x and y                                            */
+    float eps;
+    const void *x;
+    const float *weight, *bias, *residual;
+    void *y;
+    float *residual_out, *mean, *rstd;
+} ssm_norm_args;
+
+ssm_status ssm_layer_norm_fwd(const ssm_norm_args *args, void *stream);
+
+/*
+ * Backward of ssm_layer_norm_fwd. s is what was normalised: x, of dtype, or with
+ * has_residual the forward's residual_out, float32; mean and rstd are the forward's. With
+ * xh = (s - mean) rstd, g = dy weight and the means taken over the row:
+ *   ds = rstd (g - mean(g) - xh mean(g xh)) + dresidual_out
+ *   dx = ds in dtype, dresidual = ds in float32 (NULL to skip)
+ *   dweight = sum over rows of dy xh,  dbias = sum over rows of dy (NULL to skip)
+ * dresidual_out, the gradient of residual_out, may be NULL for 0. dweight and dbias are
+ * summed in float32 in an order fixed by the shape: results repeat bit for bit. No rows:
+ * dweight = dbias = 0. The workspace holds the partial sums
+ * (ssm_layer_norm_bwd_workspace_size() bytes, on 16).
+ */
+typedef struct {
+    int64_t rows, dim;
+    ssm_dtype dtype;         /* of dy, dx, and of s without has_residual              */
+    int32_t has_residual;
+    const void *s, *dy;
+    const float *weight, *mean, *rstd, *dresidual_out;
+    void *dx;
+    float *dresidual, *dweight, *dbias;
+    void *workspace;
+    size_t workspace_bytes;
+} ssm_norm_bwd_args;
+
+size_t ssm_layer_norm_bwd_workspace_size(const ssm_norm_bwd_args *args);
+ssm_status ssm_layer_norm_bwd(const ssm_norm_bwd_args *args, void *stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *ssm_status_string(ssm_status status);
 

@@ -10,7 +10,11 @@ device, the calls raise.
     y, h_last = scan_fwd(..., return_last_state=True)         # h_last [B, D, N] fp32
     y = step(x_t, dt_t, A, B_t, C_t, h, D, z_t, dt_bias)     # h [B, D, N] updated in place
     y = scan_fwd_host(x, dt, A, B, C, D, z, dt_bias)         # x, dt, z, B, C, y in host memory
+    y = gated_scan(x, r, i, lam)                             # gated linear recurrence, with its backward
+    y = gated_step(x_t, r_t, i_t, lam, h)                    # one token of it, h [B, D] updated in place
+    y, s = layer_norm(x, weight, bias, residual)             # s = x + residual, y its layer norm
 """
+import contextlib
 import ctypes
 
 import torch
@@ -19,7 +23,8 @@ from . import _native
 from ._native import SSM_A_GENERAL, SSM_DELTA_SOFTPLUS, SSM_EXACT_ZOH
 
 __all__ = ["scan_fwd", "scan_fwd_host", "scan_bwd", "selective_scan", "ssd_fwd", "step", "workspace_size",
-           "workspace_status", "ScanWorkspace"]
+           "workspace_status", "ScanWorkspace", "gated_scan", "gated_scan_fwd", "gated_scan_bwd", "gated_step",
+           "layer_norm", "layer_norm_fwd", "layer_norm_bwd"]
 
 _TOKEN_DTYPES = {torch.float32: _native.SSM_F32, torch.bfloat16: _native.SSM_BF16}
 
@@ -459,3 +464,308 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, del
     y, h_last = _SelectiveScan.apply(x, dt, A, B, C, D, z, dt_bias, h0, conv_w, conv_b, conv_x0, delta_softplus,
                                      exact_zoh)
     return (y, h_last) if return_last_state else y
+
+
+def _on_stream(stream, s, tensors):
+    """For a caller's stream: the context in which outputs and scratch are allocated (they
+    then belong to that stream), the inputs being held until the stream has read them."""
+    if stream is None or s.cuda_stream == torch.cuda.current_stream(s.device).cuda_stream:
+        return contextlib.nullcontext()
+    for t in tensors:
+        if t is not None:
+            t.record_stream(s)
+    return torch.cuda.stream(s)
+
+
+def _need_strided(t, name, shape, dtype, device):
+    """As _need, for tokens [.., D] whose channels are neighbours in memory but whose leading
+    dimensions may have any stride; returns those strides (0 where the size is 1)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device or t.device.type != "cuda":
+        raise ValueError(f"{name}: must be on {device} (a CUDA device)")
+    if shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the channels must be contiguous (stride 1 in the last dimension)")
+    return [t.stride(k) if shape[k] > 1 else 0 for k in range(len(shape) - 1)]
+
+
+def _gated_common(a, x, r, i, lam, reset, c, h0):
+    """Check and fill in what the gated scan's forward and backward take alike."""
+    dev, tok = x.device, x.dtype
+    if tok not in _TOKEN_DTYPES:
+        raise TypeError(f"x: dtype must be float32 or bfloat16, got {tok}")
+    if x.dim() != 3:
+        raise ValueError("x must be [B, L, D]")
+    Bsz, L, Dm = x.shape
+    for t, name in ((x, "x"), (r, "r"), (i, "i")):
+        getattr(a, name + "_stride")[:] = _need_strided(t, name, (Bsz, L, Dm), tok, dev)
+    _need(lam, "lam", (Dm,), torch.float32, dev)
+    if reset is not None:
+        _need(reset, "reset", (Bsz, L), torch.bool, dev)
+    if h0 is not None:
+        _need(h0, "h0", (Bsz, Dm), torch.float32, dev)
+    a.batch, a.seqlen, a.dim, a.dtype, a.flags, a.c = Bsz, L, Dm, _TOKEN_DTYPES[tok], 0, c
+    a.x, a.r, a.i, a.reset, a.lam = (_ptr(t) for t in (x, r, i, reset, lam))
+    return Bsz, L, Dm
+
+
+def _scratch(a, nbytes, workspace, dev):
+    """The call's workspace: the caller's, or fresh memory of the current stream."""
+    if workspace is None:
+        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+    else:
+        ws = workspace.get(nbytes, dev) if isinstance(workspace, ScanWorkspace) else workspace
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    a.workspace, a.workspace_bytes = _ptr(ws), ws.numel() * ws.element_size()
+    if a.workspace_bytes < nbytes:
+        raise ValueError(f"workspace too small: {a.workspace_bytes} < {nbytes} bytes")
+    return ws
+
+
+def gated_scan_fwd(x, r, i, lam, h0=None, *, reset=None, c=8.0, return_last_state=False, return_states=False,
+                   out=None, h_last=None, workspace=None, stream=None):
+    """Gated linear recurrence over whole sequences (see include/ssm_scan.h, ssm_gated_scan_fwd):
+    a_t = exp(-c softplus(lam) sigmoid(r_t)), h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t.
+
+    x, r, i: [B, L, D] float32 or bfloat16, the channels contiguous and the other strides
+    free (slices of one projection); lam: [D] float32; h0: [B, D] float32; reset: [B, L]
+    bool, true where a new document begins (the state before it is dropped and the input is
+    taken in full). Returns y [B, L, D] in x's dtype, then with return_last_state the final state
+    [B, D] float32, and with return_states the states that gated_scan_bwd takes
+    ([B, ceil(L / 64), D] float32).
+    """
+    a = _native.GatedArgs()
+    Bsz, L, Dm = _gated_common(a, x, r, i, lam, reset, c, h0)
+    dev, tok = x.device, x.dtype
+    lib = _native.lib()
+    s = _resolve_stream(stream, dev)
+    with torch.cuda.device(dev), _on_stream(stream, s, (x, r, i, lam, reset, h0, out, h_last)):
+        y = torch.empty((Bsz, L, Dm), dtype=tok, device=dev) if out is None else out
+        _need(y, "out", (Bsz, L, Dm), tok, dev)
+        if return_last_state and h_last is None:
+            h_last = torch.empty((Bsz, Dm), dtype=torch.float32, device=dev)
+        if h_last is not None:
+            _need(h_last, "h_last", (Bsz, Dm), torch.float32, dev)
+        states = _gated_states(Bsz, L, Dm, dev) if return_states else None
+        a.h0, a.y, a.h_last, a.states = (_ptr(t) for t in (h0, y, h_last, states))
+        ws = _scratch(a, int(lib.ssm_gated_scan_workspace_size(ctypes.byref(a))), workspace, dev)
+        _native.check(lib.ssm_gated_scan_fwd(ctypes.byref(a), _handle(s)), "ssm_gated_scan_fwd")
+        del ws
+    res = (y,) + ((h_last,) if return_last_state else ()) + ((states,) if return_states else ())
+    return res if len(res) > 1 else y
+
+
+def _gated_states(Bsz, L, Dm, dev):
+    return torch.empty((Bsz, -(-L // _native.SSM_GATED_CHUNK), Dm), dtype=torch.float32, device=dev)
+
+
+def gated_scan_bwd(x, r, i, lam, dy, h0=None, dh_last=None, *, states=None, reset=None, c=8.0, workspace=None,
+                   stream=None):
+    """Backward of gated_scan_fwd (see include/ssm_scan.h, ssm_gated_scan_bwd): gradients given
+    dy = dL/dy [B, L, D] (dtype of x) and optionally dh_last = dL/dh_L [B, D] float32. states:
+    what the forward returned with return_states; without them they are computed again
+    from h0 by a forward pass.
+
+    Returns a dict: dx, dr, di [B, L, D] in x's dtype, dlam [D] and dh0 [B, D] float32.
+    """
+    a = _native.GatedBwdArgs()
+    Bsz, L, Dm = _gated_common(a, x, r, i, lam, reset, c, h0)
+    dev, tok = x.device, x.dtype
+    _need(dy, "dy", (Bsz, L, Dm), tok, dev)
+    if dh_last is not None:
+        _need(dh_last, "dh_last", (Bsz, Dm), torch.float32, dev)
+    lib = _native.lib()
+    s = _resolve_stream(stream, dev)
+    with torch.cuda.device(dev), _on_stream(stream, s, (x, r, i, lam, reset, h0, dy, dh_last, states)):
+        if states is None:
+            states = _gated_states(Bsz, L, Dm, dev)
+            f = _native.GatedArgs()
+            _gated_common(f, x, r, i, lam, reset, c, h0)
+            f.h0, f.states = _ptr(h0), _ptr(states)
+            ws = _scratch(f, int(lib.ssm_gated_scan_workspace_size(ctypes.byref(f))), None, dev)
+            _native.check(lib.ssm_gated_scan_fwd(ctypes.byref(f), _handle(s)), "ssm_gated_scan_fwd")
+            del ws
+        _need(states, "states", (Bsz, -(-L // _native.SSM_GATED_CHUNK), Dm), torch.float32, dev)
+        tokens = dict(dtype=tok, device=dev)
+        g = dict(dx=torch.empty((Bsz, L, Dm), **tokens), dr=torch.empty((Bsz, L, Dm), **tokens),
+                 di=torch.empty((Bsz, L, Dm), **tokens), dlam=torch.empty((Dm,), dtype=torch.float32, device=dev),
+                 dh0=torch.empty((Bsz, Dm), dtype=torch.float32, device=dev))
+        a.states, a.dy, a.dh_last = _ptr(states), _ptr(dy), _ptr(dh_last)
+        a.dx, a.dr, a.di, a.dlam, a.dh0 = (_ptr(t) for t in g.values())
+        ws = _scratch(a, int(lib.ssm_gated_scan_bwd_workspace_size(ctypes.byref(a))), workspace, dev)
+        _native.check(lib.ssm_gated_scan_bwd(ctypes.byref(a), _handle(s)), "ssm_gated_scan_bwd")
+        del ws
+    return g
+
+
+def gated_step(x, r, i, lam, h, *, c=8.0, h_out=None, out=None, stream=None):
+    """One token of the gated linear recurrence (see include/ssm_scan.h, ssm_gated_step).
+
+    x, r, i: [B, D], the channels contiguous; lam: [D]; h: [B, D] float32, updated in place,
+    or read only when h_out [B, D] is given to take the new state. Returns y [B, D].
+    """
+    dev, tok = x.device, x.dtype
+    if tok not in _TOKEN_DTYPES:
+        raise TypeError(f"x: dtype must be float32 or bfloat16, got {tok}")
+    if x.dim() != 2:
+        raise ValueError("x must be [B, D]")
+    Bsz, Dm = x.shape
+    strides = [_need_strided(t, name, (Bsz, Dm), tok, dev)[0] for t, name in ((x, "x"), (r, "r"), (i, "i"))]
+    _need(lam, "lam", (Dm,), torch.float32, dev)
+    _need(h, "h", (Bsz, Dm), torch.float32, dev)
+    h_out = h if h_out is None else h_out
+    _need(h_out, "h_out", (Bsz, Dm), torch.float32, dev)
+    s = _resolve_stream(stream, dev)
+    with torch.cuda.device(dev), _on_stream(stream, s, (x, r, i, lam, h, h_out, out)):
+        y = torch.empty((Bsz, Dm), dtype=tok, device=dev) if out is None else out
+        _need(y, "out", (Bsz, Dm), tok, dev)
+        rc = _native.lib().ssm_gated_step(Bsz, Dm, _TOKEN_DTYPES[tok], c, _ptr(x), strides[0], _ptr(r), strides[1],
+                                          _ptr(i), strides[2], _ptr(lam), _ptr(h), _ptr(h_out), _ptr(y), _handle(s))
+    _native.check(rc, "ssm_gated_step")
+    return y
+
+
+class _GatedScan(torch.autograd.Function):
+    """gated_scan_fwd as an autograd function; of the forward it keeps the inputs and the
+    states before every chunk."""
+
+    @staticmethod
+    def forward(ctx, x, r, i, lam, h0, reset, c, last):
+        ctx.set_materialize_grads(False)
+        res = gated_scan_fwd(x, r, i, lam, h0, reset=reset, c=c, return_last_state=last, return_states=True)
+        ctx.save_for_backward(x, r, i, lam, reset, res[-1])
+        ctx.c, ctx.has_h0 = c, h0 is not None
+        return res[:-1] if last else res[0]
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dh_last=None):
+        x, r, i, lam, reset, states = ctx.saved_tensors
+        if dy is None and dh_last is None:
+            return (None,) * 8
+        dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.to(x.dtype).contiguous()
+        dh_last = None if dh_last is None else dh_last.float().contiguous()
+        g = gated_scan_bwd(x, r, i, lam, dy, None, dh_last, states=states, reset=reset, c=ctx.c)
+        return g["dx"], g["dr"], g["di"], g["dlam"], g["dh0"] if ctx.has_h0 else None, None, None, None
+
+
+def gated_scan(x, r, i, lam, h0=None, *, reset=None, c=8.0, return_last_state=False):
+    """The gated linear recurrence with its backward attached for torch.autograd: y (and the
+    final state) from gated_scan_fwd; gradients for x, r, i, lam and h0 from gated_scan_bwd."""
+    return _GatedScan.apply(x, r, i, lam, h0, reset, c, return_last_state)
+
+
+def _norm_shape(t, name):
+    if t.dtype not in _TOKEN_DTYPES:
+        raise TypeError(f"{name}: dtype must be float32 or bfloat16, got {t.dtype}")
+    if t.dim() < 1:
+        raise ValueError(f"{name} must be [..., D]")
+    Dm = t.shape[-1]
+    return (t.numel() // Dm if Dm else 0), Dm
+
+
+def layer_norm_fwd(x, weight, bias=None, residual=None, *, eps=1e-5, out=None, residual_out=None,
+                   return_stats=False, stream=None):
+    """Layer norm of the rows of x, or of x + residual (see include/ssm_scan.h, ssm_layer_norm_fwd).
+
+    x: [..., D] float32 or bfloat16, D at most 16384; weight, bias: [D] float32; residual: [..., D]
+    float32, the residual stream. Returns y in x's dtype; with a residual also s = x +
+    residual in float32 (residual_out, which may be residual itself); with return_stats also the
+    rows' mean and 1 / sqrt(var + eps), float32.
+    """
+    dev, tok = x.device, x.dtype
+    rows, Dm = _norm_shape(x, "x")
+    _need(x, "x", x.shape, tok, dev)
+    _need(weight, "weight", (Dm,), torch.float32, dev)
+    if bias is not None:
+        _need(bias, "bias", (Dm,), torch.float32, dev)
+    if residual is not None:
+        _need(residual, "residual", x.shape, torch.float32, dev)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs residual")
+    s = _resolve_stream(stream, dev)
+    with torch.cuda.device(dev), _on_stream(stream, s, (x, weight, bias, residual, out, residual_out)):
+        y = torch.empty_like(x) if out is None else out
+        _need(y, "out", x.shape, tok, dev)
+        if residual is not None:
+            residual_out = torch.empty_like(residual) if residual_out is None else residual_out
+            _need(residual_out, "residual_out", x.shape, torch.float32, dev)
+        stats = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=dev) if return_stats else (None, None)
+        a = _native.NormArgs()
+        a.rows, a.dim, a.dtype, a.eps = rows, Dm, _TOKEN_DTYPES[tok], eps
+        a.x, a.weight, a.bias, a.residual, a.y, a.residual_out, a.mean, a.rstd = (
+            _ptr(t) for t in (x, weight, bias, residual, y, residual_out, stats[0], stats[1]))
+        _native.check(_native.lib().ssm_layer_norm_fwd(ctypes.byref(a), _handle(s)), "ssm_layer_norm_fwd")
+    res = (y,) + ((residual_out,) if residual is not None else ()) + ((stats[0], stats[1]) if return_stats else ())
+    return res if len(res) > 1 else y
+
+
+def layer_norm_bwd(dy, s, weight, mean, rstd, dresidual_out=None, *, residual=False, bias=True, workspace=None,
+                   stream=None):
+    """Backward of layer_norm_fwd (see include/ssm_scan.h, ssm_layer_norm_bwd), given dy = dL/dy [..., D].
+
+    s: what the forward normalised, x in dy's dtype or, with residual, the forward's residual_out in
+    float32; mean, rstd: the forward's; dresidual_out: the gradient of residual_out, float32.
+    Returns a dict: dx in dy's dtype; dweight and (None without bias) dbias [D] float32;
+    with residual dresidual in float32 (dx itself for float32 tokens), else None.
+    """
+    dev, tok = dy.device, dy.dtype
+    rows, Dm = _norm_shape(dy, "dy")
+    f32 = torch.float32
+    _need(dy, "dy", dy.shape, tok, dev)
+    _need(s, "s", dy.shape, f32 if residual else tok, dev)
+    _need(weight, "weight", (Dm,), f32, dev)
+    _need(mean, "mean", dy.shape[:-1], f32, dev)
+    _need(rstd, "rstd", dy.shape[:-1], f32, dev)
+    if dresidual_out is not None:
+        if not residual:
+            raise ValueError("dresidual_out needs residual")
+        _need(dresidual_out, "dresidual_out", dy.shape, f32, dev)
+    lib = _native.lib()
+    st = _resolve_stream(stream, dev)
+    with torch.cuda.device(dev), _on_stream(stream, st, (dy, s, weight, mean, rstd, dresidual_out)):
+        dx = torch.empty_like(dy)
+        two = residual and tok != f32
+        dres = torch.empty(dy.shape, dtype=f32, device=dev) if two else None
+        dweight = torch.empty((Dm,), dtype=f32, device=dev)
+        dbias = torch.empty((Dm,), dtype=f32, device=dev) if bias else None
+        a = _native.NormBwdArgs()
+        a.rows, a.dim, a.dtype, a.has_residual = rows, Dm, _TOKEN_DTYPES[tok], int(residual)
+        a.s, a.dy, a.weight, a.mean, a.rstd, a.dresidual_out, a.dx, a.dresidual, a.dweight, a.dbias = (
+            _ptr(t) for t in (s, dy, weight, mean, rstd, dresidual_out, dx, dres, dweight, dbias))
+        ws = _scratch(a, int(lib.ssm_layer_norm_bwd_workspace_size(ctypes.byref(a))), workspace, dev)
+        _native.check(lib.ssm_layer_norm_bwd(ctypes.byref(a), _handle(st)), "ssm_layer_norm_bwd")
+        del ws
+    return dict(dx=dx, dweight=dweight, dbias=dbias, dresidual=(dres if two else dx) if residual else None)
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, eps):
+        ctx.set_materialize_grads(False)
+        res = layer_norm_fwd(x, weight, bias, residual, eps=eps, return_stats=True)
+        ctx.save_for_backward(x if residual is None else res[1], weight, res[-2], res[-1])
+        ctx.has_bias, ctx.residual, ctx.tok = bias is not None, residual is not None, x.dtype
+        return res[0] if residual is None else res[:2]
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, ds=None):
+        s, weight, mean, rstd = ctx.saved_tensors
+        if dy is None and ds is None:
+            return (None,) * 5
+        dy = torch.zeros(s.shape, dtype=ctx.tok, device=s.device) if dy is None else dy.to(ctx.tok).contiguous()
+        ds = None if ds is None else ds.float().contiguous()
+        g = layer_norm_bwd(dy, s, weight, mean, rstd, ds, residual=ctx.residual, bias=ctx.has_bias)
+        return g["dx"], g["dweight"], g["dbias"], g["dresidual"], None
+
+
+def layer_norm(x, weight, bias=None, residual=None, *, eps=1e-5):
+    """The layer norm with its backward attached for torch.autograd: y, or with a residual
+    (y, x + residual), from layer_norm_fwd; gradients from layer_norm_bwd."""
+    return _LayerNorm.apply(x, weight, bias, residual, eps)

@@ -12,6 +12,7 @@ SSM_A_GENERAL = 2
 SSM_EXACT_ZOH = 4
 SSM_SEQ_PARALLEL = 8
 SSM_SEQ_HANDOFF = 16
+SSM_GATED_CHUNK = 64
 SSM_TEST_SHORT_SEGMENTS = 0x40000000
 SSM_TEST_DROP_HANDOFF = 0x80000000
 
@@ -19,7 +20,9 @@ SSM_TEST_DROP_HANDOFF = 0x80000000
 EXPORTS = ("ssm_scan_workspace_size", "ssm_scan_fwd", "ssm_step", "ssm_step_conv", "ssm_workspace_status",
            "ssm_status_string", "ssm_scan_fwd_noalloc", "ssm_noalloc_status", "ssm_scan_host_staging_size",
            "ssm_scan_fwd_host", "ssm_scan_bwd_workspace_size", "ssm_scan_bwd", "ssm_ssd_workspace_size",
-           "ssm_ssd_fwd")
+           "ssm_ssd_fwd", "ssm_gated_states_size", "ssm_gated_scan_workspace_size", "ssm_gated_scan_fwd",
+           "ssm_gated_scan_bwd_workspace_size", "ssm_gated_scan_bwd", "ssm_gated_step", "ssm_layer_norm_fwd",
+           "ssm_layer_norm_bwd_workspace_size", "ssm_layer_norm_bwd")
 
 
 class ScanArgs(ctypes.Structure):
@@ -62,6 +65,48 @@ class SsdArgs(ctypes.Structure):
     ]
 
 
+class GatedArgs(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64), ("dtype", ctypes.c_int),
+        ("flags", ctypes.c_uint32), ("c", ctypes.c_float), ("x", ctypes.c_void_p), ("r", ctypes.c_void_p),
+        ("i", ctypes.c_void_p), ("x_stride", ctypes.c_int64 * 2), ("r_stride", ctypes.c_int64 * 2),
+        ("i_stride", ctypes.c_int64 * 2), ("reset", ctypes.c_void_p), ("lam", ctypes.c_void_p),
+        ("h0", ctypes.c_void_p), ("y", ctypes.c_void_p), ("h_last", ctypes.c_void_p), ("states", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class GatedBwdArgs(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64), ("dtype", ctypes.c_int),
+        ("flags", ctypes.c_uint32), ("c", ctypes.c_float), ("x", ctypes.c_void_p), ("r", ctypes.c_void_p),
+        ("i", ctypes.c_void_p), ("x_stride", ctypes.c_int64 * 2), ("r_stride", ctypes.c_int64 * 2),
+        ("i_stride", ctypes.c_int64 * 2), ("reset", ctypes.c_void_p), ("lam", ctypes.c_void_p),
+        ("states", ctypes.c_void_p), ("dy", ctypes.c_void_p), ("dh_last", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+        ("dr", ctypes.c_void_p), ("di", ctypes.c_void_p), ("dlam", ctypes.c_void_p), ("dh0", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class NormArgs(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("dtype", ctypes.c_int), ("eps", ctypes.c_float),
+        ("x", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p), ("y", ctypes.c_void_p), ("residual_out", ctypes.c_void_p),
+        ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+    ]
+
+
+class NormBwdArgs(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("dtype", ctypes.c_int), ("has_residual", ctypes.c_int32),
+        ("s", ctypes.c_void_p), ("dy", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("mean", ctypes.c_void_p),
+        ("rstd", ctypes.c_void_p), ("dresidual_out", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+        ("dresidual", ctypes.c_void_p), ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 _lib = None
 
 
@@ -100,6 +145,24 @@ def lib():
         L.ssm_scan_bwd.restype = ctypes.c_int
         L.ssm_workspace_status.argtypes = [vp, vp]
         L.ssm_workspace_status.restype = ctypes.c_int
+        L.ssm_gated_states_size.argtypes = [i64, i64, i64]
+        L.ssm_gated_states_size.restype = ctypes.c_size_t
+        L.ssm_gated_scan_workspace_size.argtypes = [ctypes.POINTER(GatedArgs)]
+        L.ssm_gated_scan_workspace_size.restype = ctypes.c_size_t
+        L.ssm_gated_scan_fwd.argtypes = [ctypes.POINTER(GatedArgs), vp]
+        L.ssm_gated_scan_fwd.restype = ctypes.c_int
+        L.ssm_gated_scan_bwd_workspace_size.argtypes = [ctypes.POINTER(GatedBwdArgs)]
+        L.ssm_gated_scan_bwd_workspace_size.restype = ctypes.c_size_t
+        L.ssm_gated_scan_bwd.argtypes = [ctypes.POINTER(GatedBwdArgs), vp]
+        L.ssm_gated_scan_bwd.restype = ctypes.c_int
+        L.ssm_gated_step.argtypes = [i64, i64, ctypes.c_int, ctypes.c_float] + [vp, i64] * 3 + [vp] * 5
+        L.ssm_gated_step.restype = ctypes.c_int
+        L.ssm_layer_norm_fwd.argtypes = [ctypes.POINTER(NormArgs), vp]
+        L.ssm_layer_norm_fwd.restype = ctypes.c_int
+        L.ssm_layer_norm_bwd_workspace_size.argtypes = [ctypes.POINTER(NormBwdArgs)]
+        L.ssm_layer_norm_bwd_workspace_size.restype = ctypes.c_size_t
+        L.ssm_layer_norm_bwd.argtypes = [ctypes.POINTER(NormBwdArgs), vp]
+        L.ssm_layer_norm_bwd.restype = ctypes.c_int
         L.ssm_status_string.argtypes = [ctypes.c_int]
         L.ssm_status_string.restype = ctypes.c_char_p
         _lib = L
