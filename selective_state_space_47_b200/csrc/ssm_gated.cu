@@ -9,12 +9,14 @@
 // h -> P h + H, and two such maps compose, so each thread forms the map of its K steps,
 // the warps of a block chain theirs through shared memory, and the tiles chain theirs
 // through the workspace.
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <float.h>
 #include <limits.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "../../include/ssm_scan.h"
 #include "ssm_device.cuh"
@@ -25,9 +27,9 @@ namespace {
 
 constexpr int kChunk = SSM_GATED_CHUNK;  // steps between the states kept for the backward
 constexpr int kW = 8;                    // warps of a block
-constexpr int kKF = 16;                  // steps per thread, forward
 constexpr int kKB = 8;                   // steps per thread, backward
-static_assert((kW * kKF) % kChunk == 0 && kW * kKB == kChunk, "tiles are made of whole chunks");
+static_assert(kW * kKB == kChunk, "a backward tile is a chunk");
+constexpr size_t kWsHeader = 256;
 
 // ------------------------------------------------------------- element math
 __device__ __forceinline__ float sigmoid_f(float v) { return rcp_approx(1.0f + ex2_approx(-v * kLog2e)); }
@@ -111,112 +113,530 @@ struct Shape {
     float c;
 };
 
+// ------------------------------------------------- states between blocks
+// A state handed from one block to another is a single 64-bit word beside a tag, zero until
+// written: data and flag are one access.
+__device__ __forceinline__ unsigned long long ld_word(const unsigned long long *p) {
+    unsigned long long v;
+    asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_word(unsigned long long *p, unsigned long long v) {
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+__device__ __forceinline__ unsigned long long pack(float h) { return (1ull << 32) | __float_as_uint(h); }
+
+// Waits for a word to be written. After 2 s, or once another wait has given up, it sets the
+// status and returns the zero word (the call's outputs are then not valid).
+__device__ __noinline__ unsigned long long wait_slow(const unsigned long long *p, unsigned int *status) {
+    const uint64_t t = globaltimer_ns();
+    for (;;) {
+        for (int k = 0; k < 64; ++k) {
+            const unsigned long long v = ld_word(p);
+            if (v != 0) return v;
+        }
+        if (globaltimer_ns() - t > 2000000000ull || *reinterpret_cast<volatile unsigned int *>(status) != 0) {
+            atomicExch(status, unsigned(SSM_ERR_TIMEOUT));
+            return 0;
+        }
+    }
+}
+__device__ __forceinline__ unsigned long long wait_word(const unsigned long long *p, unsigned int *status) {
+    const unsigned long long v = ld_word(p);
+    return v != 0 ? v : wait_slow(p, status);
+}
+
+// Pairs of neighbouring channels go through the packed float32 instructions: one issue
+// slot for both, each rounded as the scalar instruction rounds.
+__device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+    const float2 t = mul2(v, two(-kLog2e));
+    const float2 f = add2(two(1.0f), make_float2(ex2_approx(t.x), ex2_approx(t.y)));
+    return make_float2(rcp_approx(f.x), rcp_approx(f.y));
+}
+__device__ __forceinline__ float2 small_e2(float2 w) {
+    float2 q = fma2(w, two(-0.0011642870f), two(0.0082382215f));
+    q = fma2(w, q, two(-0.041649930f));
+    q = fma2(w, q, two(0.16666563f));
+    q = fma2(w, q, two(-0.5f));
+    return mul2(w, fma2(w, q, two(1.0f)));
+}
+// SMALL: w < 1/2 is known (the rate itself is below 1/2).
+template <bool SMALL>
+__device__ __forceinline__ float2 decay2(float2 w, float2 &e) {
+    if constexpr (SMALL) {
+        e = small_e2(w);
+        return fma2(e, two(-1.0f), two(1.0f));
+    } else {
+        float2 a;
+        a.x = decay(w.x, e.x);
+        a.y = decay(w.y, e.y);
+        return a;
+    }
+}
+__device__ __forceinline__ float sqrt_approx(float v) {
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float2 load2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
+__device__ __forceinline__ float2 load2(const __nv_bfloat16 *p) {
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ void store2(float *p, float2 v) { *reinterpret_cast<float2 *>(p) = v; }
+__device__ __forceinline__ void store2(__nv_bfloat16 *p, float2 v) { *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v.x, v.y); }
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Bounded wait for a phase of an mbarrier; false once any wait of the block has given up.
+__device__ __noinline__ bool wait_phase_slow(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned int *status) {
+    const uint64_t t = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort) return false;
+        if (globaltimer_ns() - t > 4000000000ull) {
+            *abort = 1;
+            atomicExch(status, unsigned(SSM_ERR_TIMEOUT));
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned int *status) {
+    return mbar_try_wait(bar, parity) || wait_phase_slow(bar, parity, abort, status);
+}
+// The same for copies in flight when the block gives up.
+__device__ __noinline__ void wait_landed(uint64_t *bar, uint32_t parity) {
+    const uint64_t t = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t < 1000000000ull) {
+    }
+}
+// Barrier of the warps that compute; true in all of them if `ok` in all.
+__device__ __forceinline__ bool compute_sync(bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(uint32_t(ok)), "n"(kW * 32)
+        : "memory");
+    return all != 0;
+}
+
 // ------------------------------------------------------------------- forward
+constexpr int kMaxCluster = 8;
+constexpr int kStages = 2;
+constexpr int kItemSlots = 8;
+
+// How a call's time is dealt out. A column (64 channels of one sequence) is walked by a cluster
+// of `cluster` blocks, which take neighbouring tiles of W K steps at a time; an item is a
+// segment of `iters` such rounds of one column.
+struct Plan {
+    int64_t columns, rounds;  // rounds of a column: ceil(tiles / cluster)
+    int cluster, iters, segs;
+    unsigned int items;
+    bool local;               // one pass for the segments' maps before the pass that writes
+    int grid;
+};
+
 template <typename T>
 struct FwdArgs {
     Shape s;
+    Plan pl;
+    unsigned int *counter, *status;
+    unsigned long long *starts;  // [segs][B D] states entering the segments
+    Map *maps;                   // [segs][B D] the segments' maps (local pass)
     const T *x, *r, *i;
     int64_t xb, xt, rb, rt, ib, it;
     const uint8_t *reset;
     const float *lam, *h0;
     T *y;
-    float *h_last, *states, *starts;
-    Map *maps;
+    float *h_last, *states;
 };
 
-// MAIN false: the map of every tile into maps; true: outputs, from the state before every tile in starts.
-template <typename T, int V, bool MAIN>
-__global__ void __launch_bounds__(kW * 32) gated_fwd_kernel(const FwdArgs<T> p) {
-    constexpr int K = kKF;
-    __shared__ Map sm[kW][V][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t g = blockIdx.x % p.s.groups, jb = blockIdx.x / p.s.groups;
-    const int64_t b = jb % p.s.B, j = jb / p.s.B;
-    const int64_t d = (g * 32 + lane) * V;
-    const int64_t t0 = (j * kW + warp) * K;
-    const bool on = d < p.s.D;
-    const int n = int(max(int64_t(0), min(int64_t(K), p.s.L - t0)));
+struct TileInfo {
+    unsigned int col, seg;
+    int tile;   // of the column; -1: no more
+    int flags;  // 1: first of its item, 2: last of its item
+};
 
-    float a[K][V], h[K][V];
-    float rt[V];
+template <typename T, int K>
+struct FwdShared {
+    T stage[kStages][3][kW * K][64];       // x, r, i of a tile
+    float4 maps[2][kW - 1][32];            // the warps' maps: P, H of a lane's two channels
+    float4 inbox[2][kMaxCluster][32];      // the blocks' maps of a round, from the whole cluster
+    float rate[kStages][64], start[2][64];
+    TileInfo tile[4];
+    uint64_t full[kStages], empty[kStages], mail[2], ready[2], told[kItemSlots];
+    unsigned int item[kItemSlots];
+    int abort;
+};
+
+struct Maps3 {
+    CUtensorMap x, r, i;
+};
+
+enum Load { kTma, kAsync, kPlain };  // 16-byte rows; pieces of 4 or 8 bytes; elements of 2 bytes
+
+// Decays and inputs of a thread's steps, and their map. FAST: every rate is below 1/2 (the
+// decay's exponential is not needed) and one reciprocal serves both sigmoids:
+// 1/(1+E) = (1+F)/((1+E)(1+F)); `big` tells of exponents that could overflow the product.
+template <typename T, int K, bool FAST>
+__device__ __forceinline__ float4 fwd_steps_of(const T *x, const T *r, const T *i, const float2 rt, const unsigned int fresh,
+                                               float2 (&a)[K], float2 (&h)[K], float &big) {
+    float2 P = two(1.0f), H = two(0.0f);
+    float top = -1.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) rt[v] = on ? rate(p.lam[d + v], p.s.c) : 0.0f;
-    bool cut = false;
-    {
-        Vec<T, V> xv[K], rv[K], iv[K];
-        const T *xp = p.x + b * p.xb + t0 * p.xt + d, *rp = p.r + b * p.rb + t0 * p.rt + d,
-                *ip = p.i + b * p.ib + t0 * p.it + d;
+    for (int k = 0; k < K; ++k) {
+        float2 sr, si, e;
+        if constexpr (FAST) {
+            const float2 tr = mul2(load2(r + k * 64), two(-kLog2e)), ti = mul2(load2(i + k * 64), two(-kLog2e));
+            top = fmaxf(fmaxf(top, fmaxf(tr.x, tr.y)), fmaxf(ti.x, ti.y));
+            const float2 fr = add2(two(1.0f), make_float2(ex2_approx(tr.x), ex2_approx(tr.y)));
+            const float2 fi = add2(two(1.0f), make_float2(ex2_approx(ti.x), ex2_approx(ti.y)));
+            const float2 pr = mul2(fr, fi), rc = make_float2(rcp_approx(pr.x), rcp_approx(pr.y));
+            sr = mul2(rc, fi);
+            si = mul2(rc, fr);
+        } else {
+            sr = sigmoid2(load2(r + k * 64));
+            si = sigmoid2(load2(i + k * 64));
+        }
+        a[k] = decay2<FAST>(mul2(rt, sr), e);
+        const float2 sq = mul2(e, fma2(e, two(-1.0f), two(2.0f)));
+        const float2 u = mul2(si, load2(x + k * 64));
+        h[k] = mul2(make_float2(sqrt_approx(sq.x), sqrt_approx(sq.y)), u);
+        if (fresh >> k & 1) h[k] = u;
+        P = mul2(P, a[k]);
+        H = (fresh >> k & 1) ? h[k] : fma2(a[k], H, h[k]);
+    }
+    big = top;
+    return make_float4(fresh ? 0.0f : keep(P.x), H.x, fresh ? 0.0f : keep(P.y), H.y);
+}
+__device__ __forceinline__ float2 apply2(const float4 m, const float2 h) {
+    return make_float2(apply(Map{m.x, m.y}, h.x), apply(Map{m.z, m.w}, h.y));
+}
+__device__ __forceinline__ float4 then2(const float4 f, const float4 g) {
+    const Map a = then(Map{f.x, f.y}, Map{g.x, g.y}), b = then(Map{f.z, f.w}, Map{g.z, g.w});
+    return make_float4(a.P, a.H, b.P, b.H);
+}
+
+// ---------------------------------------------------------- cluster plumbing
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+// Stores into a block of the cluster that complete a transaction on that block's barrier.
+__device__ __forceinline__ void send16(uint32_t dst, float4 v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
+                 "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)), "r"(__float_as_uint(v.w)), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void send4(uint32_t dst, uint32_t v, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(dst), "r"(v), "r"(bar) : "memory");
+}
+// N bytes, or N zeros (nothing is read).
+template <int N>
+__device__ __forceinline__ void copy_async(void *dst, const void *src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(N), "r"(there ? N : 0) : "memory");
+}
+// The thread's arrival on `bar`, once its cp.async copies so far have landed.
+__device__ __forceinline__ void copy_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+template <Load LOAD>
+constexpr int kLoaders = LOAD == kTma ? 1 : 4;  // loading warps
+
+// Rows w, w + 4, ... of a tile of one tensor, by one of four loading warps; zeros past the
+// last step and the last channel, as TMA fills them. PAIRS: a lane's two channels lie on
+// their own size; else channels lane and lane + 32 come one by one.
+template <typename T, int ROWS, Load LOAD>
+__device__ __forceinline__ void load_rows(T (*dst)[64], const T *src, const int64_t stride, const int steps, const int64_t width,
+                                          const bool pairs, const int w, const int lane) {
+    if constexpr (LOAD == kAsync) {
+        if (pairs) {
+            const bool on = lane * 2 < width;
+            const T *q = src + w * stride + lane * 2;
+#pragma unroll 4
+            for (int k = w; k < ROWS; k += 4, q += 4 * stride) copy_async<2 * sizeof(T)>(&dst[k][lane * 2], on && k < steps ? q : src, on && k < steps);
+        } else if constexpr (sizeof(T) == 4) {
+            const bool on0 = lane < width, on1 = lane + 32 < width;
+            const T *q = src + w * stride + lane;
+#pragma unroll 4
+            for (int k = w; k < ROWS; k += 4, q += 4 * stride) {
+                copy_async<4>(&dst[k][lane], on0 && k < steps ? q : src, on0 && k < steps);
+                copy_async<4>(&dst[k][lane + 32], on1 && k < steps ? q + 32 : src, on1 && k < steps);
+            }
+        }
+    } else {
+        constexpr int N = 8;
+        const bool on0 = lane < width, on1 = lane + 32 < width;
+        const T *q = src + w * stride + lane;
+        for (int k0 = w; k0 < ROWS; k0 += 4 * N, q += 4 * N * stride) {
+            T v[N][2];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (on && k < n) {
-                xv[k] = ldv<T, V>(xp + k * p.xt);
-                rv[k] = ldv<T, V>(rp + k * p.rt);
-                iv[k] = ldv<T, V>(ip + k * p.it);
+            for (int n = 0; n < N; ++n) {
+                const bool in = k0 + 4 * n < steps;
+                v[n][0] = on0 && in ? q[4 * n * stride] : Tok<T>::from_f(0.0f);
+                v[n][1] = on1 && in ? q[4 * n * stride + 32] : Tok<T>::from_f(0.0f);
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                dst[k0 + 4 * n][lane] = v[n][0];
+                dst[k0 + 4 * n][lane + 32] = v[n][1];
+            }
+        }
+    }
+}
+
+// Warps 0..7 compute; warp 8 carries the state from round to round; the others load.
+//  - A computing warp turns its K steps of a tile into decays and inputs in registers and their map in
+//    shared memory; warp 7 composes the block's map and sends it to every block of the cluster.
+//  - Warp 8 has the state entering the round, and from the round's maps the one entering the
+//    block's tile and the next round. The same sums in every block: nothing comes back.
+//  - Then every computing warp knows the state entering its steps, and writes them.
+// Segments of a column are handed out in the order of time by a counter; a segment starts from
+// the state that its predecessor leaves in the workspace, which with more columns than clusters is
+// there long before (and after a local pass is always there).
+template <typename T, int K, Load LOAD>
+__global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, 2)
+    gated_fwd_kernel(const FwdArgs<T> p, const __grid_constant__ Maps3 tm, const bool pairs) {
+    static_assert(kChunk % K == 0, "a chunk starts at a warp's first step");
+    static_assert((kW * K) % 32 == 0, "the loading warps' pieces fill a tile");
+    constexpr int NL = kLoaders<LOAD>, ROWS = kW * K;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    FwdShared<T, K> &s = *reinterpret_cast<FwdShared<T, K> *>(smem_raw);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned int groups = unsigned(p.s.groups), columns = unsigned(p.pl.columns), C = unsigned(p.pl.cluster);
+    const uint32_t rank = cluster_rank();
+    const bool counted = p.pl.segs > 1 && !p.pl.local;
+    const int64_t n = p.s.B * p.s.D;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < kStages; ++k) mbar_init(&s.full[k], LOAD == kTma ? 2 : NL * 32 + 1), mbar_init(&s.empty[k], 1);
+        for (int k = 0; k < 2; ++k) mbar_init(&s.mail[k], 1), mbar_init(&s.ready[k], 1);
+        for (int k = 0; k < kItemSlots; ++k) mbar_init(&s.told[k], 1);
+        s.abort = 0;
+        fence_mbar_init();
+        if (blockIdx.x == 0 && (p.pl.segs == 1 || p.maps)) *p.status = 0;  // (else cleared with the states)
+    }
+    cluster_sync_all();
+
+    if (warp > kW) {
+        // ------------------------------------------------------------ loading
+        const int w = warp - kW - 1;
+        unsigned int it = 0;
+        for (unsigned int q = 0;; ++q) {
+            const int slot = q % kItemSlots;
+            if (w == 0 && lane == 0) {
+                mbar_arrive_expect_tx(&s.told[slot], 4);
+                if (rank == 0) {
+                    const unsigned int item = counted ? atomicAdd(p.counter, 1u) : blockIdx.x / C + q * (gridDim.x / C);
+                    for (unsigned int k = 0; k < C; ++k) send4(peer_addr(&s.item[slot], k), item, peer_addr(&s.told[slot], k));
+                }
+            }
+            bool ok = __all_sync(0xffffffffu, wait_phase(&s.told[slot], (q / kItemSlots) & 1, &s.abort, p.status));
+            const unsigned int item = s.item[slot];
+            const bool done = !ok || item >= p.pl.items;
+            const unsigned int seg = done ? 0 : item / columns, col = done ? 0 : item % columns;
+            const int r0 = int(seg) * p.pl.iters, r1 = done ? r0 + 1 : int(min(int64_t(r0 + p.pl.iters), p.pl.rounds));
+            const unsigned int g = col % groups, b = col / groups;
+            for (int round = r0; round < r1; ++round, ++it) {
+                const int st = it % kStages;
+                ok = ok && (it < kStages || wait_phase(&s.empty[st], (it / kStages - 1) & 1, &s.abort, p.status));
+                if (!__all_sync(0xffffffffu, ok)) {  // given up: not before the copies under way have landed
+                    if (LOAD == kTma)
+                        for (unsigned int k = it < kStages ? 0 : it - kStages; k < it; ++k) wait_landed(&s.full[k % kStages], (k / kStages) & 1);
+                    else
+                        asm volatile("cp.async.wait_all;" ::: "memory");
+                    goto out;
+                }
+                const int tile = round * int(C) + int(rank);
+                const int64_t t0 = int64_t(tile) * ROWS;
+                if (w == 0) {
+                    if (lane == 0)
+                        s.tile[it & 3] = {col, seg, done ? -1 : tile, (round == r0 ? 1 : 0) | (round == r1 - 1 ? 2 : 0)};
+                    if (LOAD == kTma && lane == 0) {
+                        if (done) {
+                            mbar_arrive(&s.full[st]);
+                        } else {
+                            mbar_arrive_expect_tx(&s.full[st], sizeof(s.stage[0]));
+                            tma_load_3d(s.stage[st][0], &tm.x, &s.full[st], int(g * 64), int(t0), int(b));
+                            tma_load_3d(s.stage[st][1], &tm.r, &s.full[st], int(g * 64), int(t0), int(b));
+                            tma_load_3d(s.stage[st][2], &tm.i, &s.full[st], int(g * 64), int(t0), int(b));
+                        }
+                    }
+                }
+                if (LOAD != kTma && !done) {
+                    const int steps = int(max(int64_t(0), min(int64_t(ROWS), p.s.L - t0)));
+                    const int64_t d = int64_t(g) * 64, width = p.s.D - d;
+                    load_rows<T, ROWS, LOAD>(s.stage[st][0], p.x + b * p.xb + t0 * p.xt + d, p.xt, steps, width, pairs, w, lane);
+                    load_rows<T, ROWS, LOAD>(s.stage[st][1], p.r + b * p.rb + t0 * p.rt + d, p.rt, steps, width, pairs, w, lane);
+                    load_rows<T, ROWS, LOAD>(s.stage[st][2], p.i + b * p.ib + t0 * p.it + d, p.it, steps, width, pairs, w, lane);
+                }
+                if (w == 0 && !done) {
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        const int64_t d = int64_t(g) * 64 + lane * 2 + v;
+                        s.rate[st][lane * 2 + v] = d < p.s.D ? rate(p.lam[d], p.s.c) : 0.0f;
+                    }
+                }
+                __syncwarp();
+                if (w == 0 && lane == 0) mbar_arrive(&s.full[st]);
+                if (LOAD == kAsync) {
+                    copy_async_arrive(&s.full[st]);
+                } else if (LOAD == kPlain) {
+                    mbar_arrive(&s.full[st]);
+                }
+            }
+            if (done) break;
+        }
+    } else if (warp == kW) {
+        // ---------------------------------------------------------- the carry
+        float2 S = two(0.0f);
+        float4 M = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+        for (unsigned int it = 0;; ++it) {
+            const bool ok = wait_phase(&s.full[it % kStages], (it / kStages) & 1, &s.abort, p.status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const TileInfo t = s.tile[it & 3];
+            if (t.tile < 0) break;
+            const int64_t d = int64_t(t.col % groups) * 64 + lane * 2, o = int64_t(t.col / groups) * p.s.D + d;
+            const int have = int(min(int64_t(2), p.s.D - d));  // channels of this lane (at most 2)
+            if (lane == 0) mbar_arrive_expect_tx(&s.mail[it & 1], C * sizeof(s.inbox[0][0]));
+            if (t.flags & 1) {
+                S = two(0.0f);
+                M = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+                if (!p.maps) {
+                    const unsigned long long *q = p.starts + int64_t(t.seg) * n + o;
+                    if (t.seg == 0) {
+                        if (p.h0 && have > 0) S.x = p.h0[o];
+                        if (p.h0 && have > 1) S.y = p.h0[o + 1];
+                    } else {
+                        if (have > 0) S.x = __uint_as_float(unsigned(wait_word(q, p.status)));
+                        if (have > 1) S.y = __uint_as_float(unsigned(wait_word(q + 1, p.status)));
+                    }
+                }
+            }
+            wait_phase(&s.mail[it & 1], (it >> 1) & 1, &s.abort, p.status);
+            float2 mine = S;
+            for (unsigned int k = 0; k < C; ++k) {
+                const float4 m = s.inbox[it & 1][k][lane];
+                if (k == rank) mine = S;
+                S = apply2(m, S);
+                if (p.maps) M = then2(M, m);
+            }
+            *reinterpret_cast<float2 *>(&s.start[it & 1][lane * 2]) = mine;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.ready[it & 1]);
+            if ((t.flags & 2) && rank == 0) {
+                if (p.maps) {
+                    if (have > 0) p.maps[int64_t(t.seg) * n + o] = Map{M.x, M.y};
+                    if (have > 1) p.maps[int64_t(t.seg) * n + o + 1] = Map{M.z, M.w};
+                } else if (counted && int(t.seg) + 1 < p.pl.segs) {
+                    unsigned long long *q = p.starts + int64_t(t.seg + 1) * n + o;
+                    if (have > 0) st_word(q, pack(S.x));
+                    if (have > 1) st_word(q + 1, pack(S.y));
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------- computing
+        for (unsigned int it = 0;; ++it) {
+            const int st = it % kStages;
+            const bool ok = wait_phase(&s.full[st], (it / kStages) & 1, &s.abort, p.status);
+            TileInfo t{};
+            t.tile = -1;
+            if (__all_sync(0xffffffffu, ok)) t = s.tile[it & 3];
+            if (t.tile < 0) {  // the end, or a wait that gave up: the computing warps leave together
+                compute_sync(false);
+                break;
+            }
+            const unsigned int b = t.col / groups;
+            const int64_t d = int64_t(t.col % groups) * 64 + lane * 2, o = int64_t(b) * p.s.D + d;
+            const int64_t t0 = int64_t(t.tile) * ROWS + warp * K;
+            const int steps = int(max(int64_t(0), min(int64_t(K), p.s.L - t0)));
+            unsigned int fresh = 0;
+            if (p.reset) fresh = __ballot_sync(0xffffffffu, lane < steps && p.reset[int64_t(b) * p.s.L + t0 + lane] != 0);
+            const float2 rt = *reinterpret_cast<const float2 *>(&s.rate[st][lane * 2]);
+            const T *x = &s.stage[st][0][warp * K][lane * 2], *r = &s.stage[st][1][warp * K][lane * 2],
+                    *i = &s.stage[st][2][warp * K][lane * 2];
+            float2 a[K], h[K];
+            float4 m;
+            float big = 1e30f;
+            if (__all_sync(0xffffffffu, fmaxf(rt.x, rt.y) < 0.5f)) m = fwd_steps_of<T, K, true>(x, r, i, rt, fresh, a, h, big);
+            if (__any_sync(0xffffffffu, big > 60.0f)) m = fwd_steps_of<T, K, false>(x, r, i, rt, fresh, a, h, big);
+            if (warp < kW - 1) s.maps[it & 1][warp][lane] = m;
+            if (!compute_sync(true)) break;
+            if (threadIdx.x == 0) mbar_arrive(&s.empty[st]);
+            if (warp == kW - 1) {
+                float4 all = s.maps[it & 1][0][lane];
+#pragma unroll
+                for (int w = 1; w < kW - 1; ++w) all = then2(all, s.maps[it & 1][w][lane]);
+                all = then2(all, m);
+                for (unsigned int k = 0; k < C; ++k)
+                    send16(peer_addr(&s.inbox[it & 1][rank][lane], k), all, peer_addr(&s.mail[it & 1], k));
+            }
+            wait_phase(&s.ready[it & 1], (it >> 1) & 1, &s.abort, p.status);
+            if (p.maps || d >= p.s.D || steps == 0) continue;
+            float2 hs = *reinterpret_cast<const float2 *>(&s.start[it & 1][lane * 2]);
+            for (int w = 0; w < warp; ++w) hs = apply2(s.maps[it & 1][w][lane], hs);
+            const bool both = d + 1 < p.s.D;
+            if (p.states && t0 % kChunk == 0) {
+                float *q = p.states + (int64_t(b) * ((p.s.L + kChunk - 1) / kChunk) + t0 / kChunk) * p.s.D + d;
+                q[0] = hs.x;
+                if (both) q[1] = hs.y;
+            }
+            T *yp = p.y + (int64_t(b) * p.s.L + t0) * p.s.D + d;
+            if (steps == K && p.y && pairs) {
+#pragma unroll
+                for (int k = 0; k < K; ++k, yp += p.s.D) {
+                    hs = (fresh >> k & 1) ? h[k] : fma2(a[k], hs, h[k]);
+                    store2(yp, hs);
+                }
             } else {
-                for (int v = 0; v < V; ++v) xv[k].set(v, 0.0f), rv[k].set(v, 0.0f), iv[k].set(v, 0.0f);
+#pragma unroll
+                for (int k = 0; k < K; ++k, yp += p.s.D)
+                    if (k < steps) {
+                        hs = (fresh >> k & 1) ? h[k] : fma2(a[k], hs, h[k]);
+                        if (p.y) {
+                            yp[0] = Tok<T>::from_f(hs.x);
+                            if (both) yp[1] = Tok<T>::from_f(hs.y);
+                        }
+                    }
             }
-        }
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const bool fresh = p.reset && k < n && p.reset[b * p.s.L + t0 + k];
-            cut |= fresh;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float e;
-                const float dec = decay(rt[v] * sigmoid_f(rv[k].get(v)), e);
-                const float sq = e * (2.0f - e), u = sigmoid_f(iv[k].get(v)) * xv[k].get(v);
-                a[k][v] = k < n ? (fresh ? 0.0f : dec) : 1.0f;
-                h[k][v] = k < n ? (fresh ? u : sq * inv_beta(sq) * u) : 0.0f;
+            if (p.h_last && t0 + steps == p.s.L) {
+                p.h_last[o] = hs.x;
+                if (both) p.h_last[o + 1] = hs.y;
             }
         }
     }
-    // the thread's map, and the maps of the block's warps
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        Map m{1.0f, 0.0f};
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            m.P *= a[k][v];
-            m.H = (p.reset && a[k][v] == 0.0f) ? h[k][v] : fmaf(a[k][v], m.H, h[k][v]);
-        }
-        m.P = cut ? 0.0f : keep(m.P);
-        sm[warp][v][lane] = m;
-    }
-    __syncthreads();
-    if (!MAIN) {
-        if (warp == 0 && on) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                Map m = sm[0][v][lane];
-                for (int w = 1; w < kW; ++w) m = then(m, sm[w][v][lane]);
-                p.maps[(j * p.s.B + b) * p.s.D + d + v] = m;
-            }
-        }
-        return;
-    }
-    if (!on || n == 0) return;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float hs = p.starts[(j * p.s.B + b) * p.s.D + d + v];
-        for (int w = 0; w < warp; ++w) hs = apply(sm[w][v][lane], hs);
-        if (p.states && t0 % kChunk == 0) p.states[(b * ((p.s.L + kChunk - 1) / kChunk) + t0 / kChunk) * p.s.D + d + v] = hs;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            hs = (p.reset && a[k][v] == 0.0f) ? h[k][v] : fmaf(a[k][v], hs, h[k][v]);
-            h[k][v] = hs;
-        }
-        if (p.h_last && t0 + n == p.s.L) p.h_last[b * p.s.D + d + v] = hs;
-    }
-    if (p.y) {
-        T *yp = p.y + (b * p.s.L + t0) * p.s.D + d;
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (k < n) {
-                Vec<T, V> o;
-                for (int v = 0; v < V; ++v) o.set(v, h[k][v]);
-                stv<T, V>(yp + k * p.s.D, o);
-            }
-        }
+out:
+    __syncwarp();
+    cluster_sync_all();  // no block leaves while another may still write to it
+}
+
+// The states entering the segments, from their maps.
+__global__ void __launch_bounds__(128)
+    gated_starts_kernel(int64_t n, int segs, const float *__restrict__ h0, const Map *__restrict__ maps, unsigned long long *__restrict__ starts) {
+    const int64_t k = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (k >= n) return;
+    float h = h0 ? h0[k] : 0.0f;
+#pragma unroll 8
+    for (int s = 0; s + 1 < segs; ++s) {
+        h = apply(maps[s * n + k], h);
+        starts[(s + 1) * n + k] = pack(h);
     }
 }
 
@@ -449,23 +869,155 @@ bool even(const int64_t *s) { return s[0] % 2 == 0 && s[1] % 2 == 0; }
 
 ssm_status launched() { return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA; }
 
-template <typename T, int V>
+// Segments a column's time may be cut into: enough to deal the columns out evenly.
+int max_segs(int64_t columns, int64_t chunks) { return int(std::max<int64_t>(1, std::min<int64_t>(chunks, std::max<int64_t>(8, std::min<int64_t>(256, 4096 / columns))))); }
+
+size_t carry_bytes(int64_t B, int64_t L, int64_t D) {
+    const int64_t segs = max_segs(B * ceil_div(D, 64), ceil_div(L, kChunk));
+    return kWsHeader + 2 * up256(size_t(B) * size_t(D) * size_t(segs) * 8);
+}
+
+// Clusters of each size that the GPU holds at once (0: not asked yet), by device.
+struct Residency {
+    std::atomic<int> n[64][4];
+};
+int clusters_resident(Residency &r, const void *kernel, int threads, size_t smem, int log2c) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = r.n[dev][log2c].load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(1u << log2c), cfg.blockDim = dim3(unsigned(threads)), cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute at;
+        at.id = cudaLaunchAttributeClusterDimension;
+        at.val.clusterDim.x = 1u << log2c, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+        cfg.attrs = &at, cfg.numAttrs = 1;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0)
+            return 0;
+        r.n[dev][log2c].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+// Chooses the cluster size and the segments. One unit of cost is a round (a tile in every resident
+// block). With more columns than clusters the columns' segments are dealt out in turn,
+// in as many pieces as even out the last turn; with fewer, larger clusters share a column
+// (each doubling costs a little for the slowest of more blocks), and with very few the segments
+// run side by side in two passes (twice the rounds, three launches).
+bool make_plan(Plan &pl, Residency &r, const void *kernel, int threads, size_t smem, int64_t columns, int64_t tiles, int most_segs) {
+    double best = 1e300;
+    pl.columns = columns;
+    for (int k = 0; (1 << k) <= kMaxCluster; ++k) {
+        const int c = 1 << k;
+        if (c > 1 && c / 2 >= tiles) break;
+        const int n = clusters_resident(r, kernel, threads, smem, k);
+        if (n <= 0) return false;
+        const int64_t rounds = ceil_div(tiles, c);
+        const auto consider = [&](int64_t iters, bool local, double cost) {
+            if (cost >= best) return;
+            best = cost;
+            pl.cluster = c, pl.rounds = rounds, pl.iters = int(iters), pl.segs = int(ceil_div(rounds, iters)), pl.local = local;
+            pl.items = unsigned(columns * pl.segs);
+            pl.grid = int(std::min<int64_t>(n, pl.items)) * c;
+        };
+        const double per = 1.0 + 0.03 * k;
+        consider(rounds, false, double(ceil_div(columns, n)) * double(rounds) * per);
+        for (int64_t segs = 2; segs <= std::min<int64_t>(most_segs, rounds); ++segs) {
+            const int64_t iters = ceil_div(rounds, segs), items = columns * ceil_div(rounds, iters);
+            if (columns >= n) consider(iters, false, double(ceil_div(items, n)) * double(iters) * per + 1.0);
+            if (c == 1) consider(iters, true, 2.0 * double(ceil_div(items, n)) * double(iters) + 6.0);
+        }
+    }
+    return true;
+}
+
+template <typename T, int K, Load LOAD>
+ssm_status launch_fwd(FwdArgs<T> p, const Maps3 &tm, bool pairs, cudaStream_t st) {
+    static Residency resident;
+    constexpr size_t smem = sizeof(FwdShared<T, K>);
+    constexpr int threads = (kW + 1 + kLoaders<LOAD>) * 32;
+    const auto kernel = gated_fwd_kernel<T, K, LOAD>;
+    const int64_t columns = p.s.B * p.s.groups, n = p.s.B * p.s.D;
+    const int segs = max_segs(columns, ceil_div(p.s.L, kChunk));
+    if (!make_plan(p.pl, resident, reinterpret_cast<const void *>(kernel), threads, smem, columns, ceil_div(p.s.L, kW * K), segs))
+        return SSM_ERR_CUDA;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess) return SSM_ERR_CUDA;
+    unsigned char *ws = reinterpret_cast<unsigned char *>(p.counter);
+    p.status = p.counter + 1;
+    p.starts = reinterpret_cast<unsigned long long *>(ws + kWsHeader);
+    Map *maps = reinterpret_cast<Map *>(ws + kWsHeader + up256(size_t(n) * size_t(segs) * 8));
+    if (p.pl.segs > 1 && !p.pl.local && cudaMemsetAsync(ws, 0, kWsHeader + size_t(n) * size_t(p.pl.segs) * 8, st) != cudaSuccess)
+        return SSM_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(p.pl.grid)), cfg.blockDim = dim3(unsigned(threads)), cfg.dynamicSmemBytes = smem, cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = unsigned(p.pl.cluster), at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+    cfg.attrs = &at, cfg.numAttrs = 1;
+    if (p.pl.local) {
+        p.maps = maps;
+        if (cudaLaunchKernelEx(&cfg, kernel, p, tm, pairs) != cudaSuccess) return SSM_ERR_CUDA;
+        p.maps = nullptr;
+        gated_starts_kernel<<<unsigned(ceil_div(n, 128)), 128, 0, st>>>(n, p.pl.segs, p.h0, maps, p.starts);
+    }
+    if (cudaLaunchKernelEx(&cfg, kernel, p, tm, pairs) != cudaSuccess) return SSM_ERR_CUDA;
+    return launched();
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (!fn) {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    }
+    return fn;
+}
+
+// Tokens [B, L, D] with the strides of the call, in boxes of 64 channels by `rows` steps. False where TMA cannot
+// take them: a base off 16 bytes, a stride that is not a multiple of 16 bytes or makes rows overlap.
+bool token_map(CUtensorMap *m, const void *ptr, ssm_dtype dt, int64_t B, int64_t L, int64_t D, const int64_t *stride, int rows) {
+    const int64_t es = dt == SSM_BF16 ? 2 : 4;
+    const int64_t st = L > 1 ? stride[1] * es : (D * es + 15) / 16 * 16;
+    const int64_t sb = B > 1 ? stride[0] * es : st;
+    if ((reinterpret_cast<uintptr_t>(ptr) & 15) || st % 16 || sb % 16 || st < D * es || sb < st || st >= (int64_t(1) << 40) ||
+        sb >= (int64_t(1) << 40) || B > INT_MAX || L > INT_MAX - 1024 || D > INT_MAX - 1024)
+        return false;
+    auto enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(L), cuuint64_t(B)};
+    cuuint64_t strides[2] = {cuuint64_t(st), cuuint64_t(sb)};
+    cuuint32_t box[3] = {64, cuuint32_t(rows), 1}, ones[3] = {1, 1, 1};
+    return enc(m, dt == SSM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void *>(ptr),
+               dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T>
 ssm_status run_fwd(const ssm_gated_args *a, cudaStream_t st) {
-    FwdArgs<T> p;
-    p.s = {a->batch, a->seqlen, a->dim, ceil_div(a->dim, 32 * V), ceil_div(a->seqlen, kW * kKF), a->c};
+    constexpr size_t es = sizeof(T);
+    FwdArgs<T> p = {};
+    p.s = {a->batch, a->seqlen, a->dim, ceil_div(a->dim, 64), 0, a->c};
+    p.counter = static_cast<unsigned int *>(a->workspace);
     p.x = static_cast<const T *>(a->x), p.r = static_cast<const T *>(a->r), p.i = static_cast<const T *>(a->i);
     p.xb = a->x_stride[0], p.xt = a->x_stride[1], p.rb = a->r_stride[0], p.rt = a->r_stride[1];
     p.ib = a->i_stride[0], p.it = a->i_stride[1];
     p.reset = a->reset, p.lam = a->lam, p.h0 = a->h0;
     p.y = static_cast<T *>(a->y), p.h_last = a->h_last, p.states = a->states;
-    const int64_t n = a->batch * a->dim;
-    p.maps = static_cast<Map *>(a->workspace);
-    p.starts = reinterpret_cast<float *>(static_cast<unsigned char *>(a->workspace) + up256(size_t(n) * size_t(p.s.tiles) * sizeof(Map)));
-    const unsigned grid = unsigned(a->batch * p.s.groups * p.s.tiles);
-    gated_fwd_kernel<T, V, false><<<grid, kW * 32, 0, st>>>(p);
-    gated_chain_kernel<<<unsigned(ceil_div(n, 128)), 128, 0, st>>>(n, p.s.tiles, false, a->h0, p.maps, p.starts);
-    gated_fwd_kernel<T, V, true><<<grid, kW * 32, 0, st>>>(p);
-    return launched();
+    const bool pairs = a->dim % 2 == 0 && even(a->x_stride) && even(a->r_stride) && even(a->i_stride) && aligned(a->x, 2 * es) &&
+                       aligned(a->r, 2 * es) && aligned(a->i, 2 * es) && aligned(a->y, 2 * es);
+    constexpr int KT = es == 2 ? 16 : 8;
+    Maps3 tm = {};
+    if (pairs && token_map(&tm.x, a->x, a->dtype, a->batch, a->seqlen, a->dim, a->x_stride, kW * KT) &&
+        token_map(&tm.r, a->r, a->dtype, a->batch, a->seqlen, a->dim, a->r_stride, kW * KT) &&
+        token_map(&tm.i, a->i, a->dtype, a->batch, a->seqlen, a->dim, a->i_stride, kW * KT))
+        return launch_fwd<T, KT, kTma>(p, tm, pairs, st);
+    if (pairs || es == 4) return launch_fwd<T, 8, kAsync>(p, tm, pairs, st);
+    if constexpr (es == 2) return launch_fwd<T, 8, kPlain>(p, tm, pairs, st);
+    return SSM_ERR_UNSUPPORTED;
 }
 
 template <typename T, int V>
@@ -534,8 +1086,7 @@ size_t ssm_gated_states_size(int64_t batch, int64_t seqlen, int64_t dim) {
 
 size_t ssm_gated_scan_workspace_size(const ssm_gated_args *a) {
     if (check_common(a) != SSM_OK) return 0;
-    const size_t n = size_t(a->batch) * size_t(a->dim) * size_t(ceil_div(a->seqlen, kW * kKF));
-    return up256(n * sizeof(Map)) + up256(n * 4);
+    return (a->batch == 0 || a->dim == 0) ? 0 : carry_bytes(a->batch, a->seqlen, a->dim);
 }
 
 ssm_status ssm_gated_scan_fwd(const ssm_gated_args *a, void *stream) {
@@ -561,11 +1112,7 @@ ssm_status ssm_gated_scan_fwd(const ssm_gated_args *a, void *stream) {
     }
     if (!a->workspace || a->workspace_bytes < ssm_gated_scan_workspace_size(a)) return SSM_ERR_INVALID;
     if (!aligned(a->workspace, 16)) return SSM_ERR_UNSUPPORTED;
-    // two channels per lane where every access to a pair is aligned
-    const bool two = a->dim % 2 == 0 && even(a->x_stride) && even(a->r_stride) && even(a->i_stride) &&
-                     aligned(a->x, 2 * es) && aligned(a->r, 2 * es) && aligned(a->i, 2 * es) && aligned(a->y, 2 * es);
-    if (a->dtype == SSM_BF16) return two ? run_fwd<__nv_bfloat16, 2>(a, st) : run_fwd<__nv_bfloat16, 1>(a, st);
-    return two ? run_fwd<float, 2>(a, st) : run_fwd<float, 1>(a, st);
+    return a->dtype == SSM_BF16 ? run_fwd<__nv_bfloat16>(a, st) : run_fwd<float>(a, st);
 }
 
 size_t ssm_gated_scan_bwd_workspace_size(const ssm_gated_bwd_args *a) {
