@@ -27,8 +27,6 @@ namespace {
 
 constexpr int kChunk = SSM_GATED_CHUNK;  // steps between the states kept for the backward
 constexpr int kW = 8;                    // warps of a block
-constexpr int kKB = 8;                   // steps per thread, backward
-static_assert(kW * kKB == kChunk, "a backward tile is a chunk");
 constexpr size_t kWsHeader = 256;
 
 // ------------------------------------------------------------- element math
@@ -182,6 +180,11 @@ __device__ __forceinline__ float sqrt_approx(float v) {
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+__device__ __forceinline__ float rsqrt_approx(float v) {
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
 __device__ __forceinline__ float2 load2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
 __device__ __forceinline__ float2 load2(const __nv_bfloat16 *p) {
     const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
@@ -193,10 +196,23 @@ __device__ __forceinline__ void store2(__nv_bfloat16 *p, float2 v) { *reinterpre
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// Bounded wait for a phase of an mbarrier; false once any wait of the block has given up.
+// Bounded wait for a phase of an mbarrier; false once any wait of the block has given up. A
+// try sleeps until the phase completes, 20 us at most: a spinning warp would take issue slots
+// from those that compute.
+__device__ __forceinline__ bool mbar_sleep(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000)
+        : "memory");
+    return ok != 0;
+}
 __device__ __noinline__ bool wait_phase_slow(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned int *status) {
     const uint64_t t = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!mbar_sleep(bar, parity)) {
         if (*abort) return false;
         if (globaltimer_ns() - t > 4000000000ull) {
             *abort = 1;
@@ -207,7 +223,7 @@ __device__ __noinline__ bool wait_phase_slow(uint64_t *bar, uint32_t parity, vol
     return true;
 }
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *abort, unsigned int *status) {
-    return mbar_try_wait(bar, parity) || wait_phase_slow(bar, parity, abort, status);
+    return mbar_sleep(bar, parity) || wait_phase_slow(bar, parity, abort, status);
 }
 // The same for copies in flight when the block gives up.
 __device__ __noinline__ void wait_landed(uint64_t *bar, uint32_t parity) {
@@ -215,22 +231,11 @@ __device__ __noinline__ void wait_landed(uint64_t *bar, uint32_t parity) {
     while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t < 1000000000ull) {
     }
 }
-// Barrier of the warps that compute; true in all of them if `ok` in all.
-__device__ __forceinline__ bool compute_sync(bool ok) {
-    uint32_t all;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(all)
-        : "r"(uint32_t(ok)), "n"(kW * 32)
-        : "memory");
-    return all != 0;
-}
 
 // ------------------------------------------------------------------- forward
-constexpr int kMaxCluster = 8;
-constexpr int kStages = 2;
 constexpr int kItemSlots = 8;
+constexpr int kInfos = 4;
+constexpr int kStages = 2;
 
 // How a call's time is dealt out. A column (64 channels of one sequence) is walked by a cluster
 // of `cluster` blocks, which take neighbouring tiles of W K steps at a time; an item is a
@@ -266,12 +271,13 @@ struct TileInfo {
 
 template <typename T, int K>
 struct FwdShared {
+    static constexpr int kMaxCluster = sizeof(T) * K <= 16 ? 16 : 8;
     T stage[kStages][3][kW * K][64];       // x, r, i of a tile
-    float4 maps[2][kW - 1][32];            // the warps' maps: P, H of a lane's two channels
+    float4 maps[2][kW][32];                // a warp's map (P, H of a lane's two channels), then its start
     float4 inbox[2][kMaxCluster][32];      // the blocks' maps of a round, from the whole cluster
-    float rate[kStages][64], start[2][64];
-    TileInfo tile[4];
-    uint64_t full[kStages], empty[kStages], mail[2], ready[2], told[kItemSlots];
+    float rate[kStages][64];
+    TileInfo tile[kInfos];
+    uint64_t full[kStages], empty[kStages], posted[2], mail[2], ready[2], told[kItemSlots];
     unsigned int item[kItemSlots];
     int abort;
 };
@@ -282,9 +288,10 @@ struct Maps3 {
 
 enum Load { kTma, kAsync, kPlain };  // 16-byte rows; pieces of 4 or 8 bytes; elements of 2 bytes
 
-// Decays and inputs of a thread's steps, and their map. FAST: every rate is below 1/2 (the
-// decay's exponential is not needed) and one reciprocal serves both sigmoids:
-// 1/(1+E) = (1+F)/((1+E)(1+F)); `big` tells of exponents that could overflow the product.
+// Decays and inputs of a thread's steps, and their map. FAST: no reset among them, every rate
+// between 1e-18 and 1/2 (neither the decay's exponential nor a case for beta = 0 is
+// needed), and one reciprocal serves both sigmoids: 1/(1+E) = (1+F)/((1+E)(1+F)); `big`
+// tells of gates below -41, whose exponentials' product could overflow and w underflow.
 template <typename T, int K, bool FAST>
 __device__ __forceinline__ float4 fwd_steps_of(const T *x, const T *r, const T *i, const float2 rt, const unsigned int fresh,
                                                float2 (&a)[K], float2 (&h)[K], float &big) {
@@ -308,10 +315,14 @@ __device__ __forceinline__ float4 fwd_steps_of(const T *x, const T *r, const T *
         a[k] = decay2<FAST>(mul2(rt, sr), e);
         const float2 sq = mul2(e, fma2(e, two(-1.0f), two(2.0f)));
         const float2 u = mul2(si, load2(x + k * 64));
-        h[k] = mul2(make_float2(sqrt_approx(sq.x), sqrt_approx(sq.y)), u);
-        if (fresh >> k & 1) h[k] = u;
+        if constexpr (FAST)
+            h[k] = mul2(mul2(sq, make_float2(rsqrt_approx(sq.x), rsqrt_approx(sq.y))), u);
+        else
+            h[k] = mul2(make_float2(sqrt_approx(sq.x), sqrt_approx(sq.y)), u);
+        const bool fr = !FAST && (fresh >> k & 1);
+        if (fr) h[k] = u;
         P = mul2(P, a[k]);
-        H = (fresh >> k & 1) ? h[k] : fma2(a[k], H, h[k]);
+        H = fr ? h[k] : fma2(a[k], H, h[k]);
     }
     big = top;
     return make_float4(fresh ? 0.0f : keep(P.x), H.x, fresh ? 0.0f : keep(P.y), H.y);
@@ -358,56 +369,117 @@ __device__ __forceinline__ void copy_async_arrive(uint64_t *bar) {
 }
 
 template <Load LOAD>
-constexpr int kLoaders = LOAD == kTma ? 1 : 4;  // loading warps
+constexpr int kLoaders = LOAD == kTma ? 1 : 3;  // loading warps
 
-// Rows w, w + 4, ... of a tile of one tensor, by one of four loading warps; zeros past the
+// Rows w, w + NL, ... of a tile of one tensor, by one of the loading warps; zeros past the
 // last step and the last channel, as TMA fills them. PAIRS: a lane's two channels lie on
 // their own size; else channels lane and lane + 32 come one by one.
 template <typename T, int ROWS, Load LOAD>
-__device__ __forceinline__ void load_rows(T (*dst)[64], const T *src, const int64_t stride, const int steps, const int64_t width,
+__device__ __forceinline__ void load_rows(T (*dst)[64], const T *base, const int64_t at, const int64_t stride, const int steps, const int64_t width,
                                           const bool pairs, const int w, const int lane) {
+    constexpr int NL = kLoaders<LOAD>;
+    const T *src = base + at;
     if constexpr (LOAD == kAsync) {
         if (pairs) {
             const bool on = lane * 2 < width;
             const T *q = src + w * stride + lane * 2;
 #pragma unroll 4
-            for (int k = w; k < ROWS; k += 4, q += 4 * stride) copy_async<2 * sizeof(T)>(&dst[k][lane * 2], on && k < steps ? q : src, on && k < steps);
+            for (int k = w; k < ROWS; k += NL, q += NL * stride) copy_async<2 * sizeof(T)>(&dst[k][lane * 2], on && k < steps ? q : base, on && k < steps);
         } else if constexpr (sizeof(T) == 4) {
             const bool on0 = lane < width, on1 = lane + 32 < width;
             const T *q = src + w * stride + lane;
 #pragma unroll 4
-            for (int k = w; k < ROWS; k += 4, q += 4 * stride) {
-                copy_async<4>(&dst[k][lane], on0 && k < steps ? q : src, on0 && k < steps);
-                copy_async<4>(&dst[k][lane + 32], on1 && k < steps ? q + 32 : src, on1 && k < steps);
+            for (int k = w; k < ROWS; k += NL, q += NL * stride) {
+                copy_async<4>(&dst[k][lane], on0 && k < steps ? q : base, on0 && k < steps);
+                copy_async<4>(&dst[k][lane + 32], on1 && k < steps ? q + 32 : base, on1 && k < steps);
             }
         }
     } else {
         constexpr int N = 8;
         const bool on0 = lane < width, on1 = lane + 32 < width;
         const T *q = src + w * stride + lane;
-        for (int k0 = w; k0 < ROWS; k0 += 4 * N, q += 4 * N * stride) {
+        for (int k0 = w; k0 < ROWS; k0 += NL * N, q += NL * N * stride) {
             T v[N][2];
 #pragma unroll
             for (int n = 0; n < N; ++n) {
-                const bool in = k0 + 4 * n < steps;
-                v[n][0] = on0 && in ? q[4 * n * stride] : Tok<T>::from_f(0.0f);
-                v[n][1] = on1 && in ? q[4 * n * stride + 32] : Tok<T>::from_f(0.0f);
+                const bool in = k0 + NL * n < min(ROWS, steps);
+                v[n][0] = on0 && in ? q[NL * n * stride] : Tok<T>::from_f(0.0f);
+                v[n][1] = on1 && in ? q[NL * n * stride + 32] : Tok<T>::from_f(0.0f);
             }
 #pragma unroll
             for (int n = 0; n < N; ++n) {
-                dst[k0 + 4 * n][lane] = v[n][0];
-                dst[k0 + 4 * n][lane + 32] = v[n][1];
+                if (k0 + NL * n < ROWS) {
+                    dst[k0 + NL * n][lane] = v[n][0];
+                    dst[k0 + NL * n][lane + 32] = v[n][1];
+                }
             }
         }
     }
 }
 
-// Warps 0..7 compute; warp 8 carries the state from round to round; the others load.
-//  - A computing warp turns its K steps of a tile into decays and inputs in registers and their map in
-//    shared memory; warp 7 composes the block's map and sends it to every block of the cluster.
-//  - Warp 8 has the state entering the round, and from the round's maps the one entering the
-//    block's tile and the next round. The same sums in every block: nothing comes back.
+// What the loading warps do, in both directions: take items, and bring their rounds' tiles into the stages
+// through `issue` (which returns the tile's index in its column).
+template <Load LOAD, typename Args, typename Shared, typename Issue>
+__device__ __forceinline__ void load_tiles(const Args &p, Shared &s, const int w, const int lane, const uint32_t rank, const unsigned int C,
+                                           const unsigned int columns, const unsigned int groups, const bool counted, const Issue &issue) {
+    unsigned int it = 0;
+    for (unsigned int q = 0;; ++q) {
+        const int slot = q % kItemSlots;
+        if (w == 0 && lane == 0) {
+            mbar_arrive_expect_tx(&s.told[slot], 4);
+            if (rank == 0) {
+                const unsigned int item = counted ? atomicAdd(p.counter, 1u) : blockIdx.x / C + q * (gridDim.x / C);
+                for (unsigned int k = 0; k < C; ++k) send4(peer_addr(&s.item[slot], k), item, peer_addr(&s.told[slot], k));
+            }
+        }
+        bool ok = __all_sync(0xffffffffu, wait_phase(&s.told[slot], (q / kItemSlots) & 1, &s.abort, p.status));
+        const unsigned int item = s.item[slot];
+        const bool done = !ok || item >= p.pl.items;
+        const unsigned int seg = done ? 0 : item / columns, col = done ? 0 : item % columns;
+        const int r0 = int(seg) * p.pl.iters, r1 = done ? r0 + 1 : int(min(int64_t(r0 + p.pl.iters), p.pl.rounds));
+        const unsigned int g = col % groups, b = col / groups;
+        for (int round = r0; round < r1; ++round, ++it) {
+            const int st = it % kStages;
+            ok = ok && (it < kStages || wait_phase(&s.empty[st], (it / kStages - 1) & 1, &s.abort, p.status));
+            if (!__all_sync(0xffffffffu, ok)) {  // given up: not before the copies under way have landed
+                if (LOAD == kTma)
+                    for (unsigned int k = it < kStages ? 0 : it - kStages; k < it; ++k) wait_landed(&s.full[k % kStages], (k / kStages) & 1);
+                else
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                return;
+            }
+            int tile = -1;
+            if (!done)
+                tile = issue(st, g, b, round);
+            else if (LOAD == kTma && lane == 0)
+                mbar_arrive(&s.full[st]);
+            if (w == 0 && !done) {
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const int64_t d = int64_t(g) * 64 + lane * 2 + v;
+                    s.rate[st][lane * 2 + v] = d < p.s.D ? rate(p.lam[d], p.s.c) : 0.25f;
+                }
+            }
+            if (w == 0 && lane == 0) s.tile[it % kInfos] = {col, seg, tile, (round == r0 ? 1 : 0) | (round == r1 - 1 ? 2 : 0)};
+            __syncwarp();
+            if (w == 0 && lane == 0) mbar_arrive(&s.full[st]);
+            if (LOAD == kAsync)
+                copy_async_arrive(&s.full[st]);
+            else if (LOAD == kPlain)
+                mbar_arrive(&s.full[st]);
+        }
+        if (done) return;
+    }
+}
+
+// Warps 0..7 compute; warp 8 carries the state along; the others load.
+//  - A computing warp turns its K steps of a tile into decays and inputs in registers and posts
+//    their map in shared memory.
+//  - Warp 8 composes the block's map, sends it to every block of the cluster, and has from the
+//    round's maps the state entering its block's tile, each of the tile's warps and the next
+//    round. The same sums in every block: nothing comes back.
 //  - Then every computing warp knows the state entering its steps, and writes them.
+// No barrier joins the computing warps: they meet warp 8 on mbarriers only.
 // Segments of a column are handed out in the order of time by a counter; a segment starts from
 // the state that its predecessor leaves in the workspace, which with more columns than clusters is
 // there long before (and after a local pass is always there).
@@ -415,7 +487,6 @@ template <typename T, int K, Load LOAD>
 __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, 2)
     gated_fwd_kernel(const FwdArgs<T> p, const __grid_constant__ Maps3 tm, const bool pairs) {
     static_assert(kChunk % K == 0, "a chunk starts at a warp's first step");
-    static_assert((kW * K) % 32 == 0, "the loading warps' pieces fill a tile");
     constexpr int NL = kLoaders<LOAD>, ROWS = kW * K;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     FwdShared<T, K> &s = *reinterpret_cast<FwdShared<T, K> *>(smem_raw);
@@ -425,8 +496,8 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, 2)
     const bool counted = p.pl.segs > 1 && !p.pl.local;
     const int64_t n = p.s.B * p.s.D;
     if (threadIdx.x == 0) {
-        for (int k = 0; k < kStages; ++k) mbar_init(&s.full[k], LOAD == kTma ? 2 : NL * 32 + 1), mbar_init(&s.empty[k], 1);
-        for (int k = 0; k < 2; ++k) mbar_init(&s.mail[k], 1), mbar_init(&s.ready[k], 1);
+        for (int k = 0; k < kStages; ++k) mbar_init(&s.full[k], LOAD == kTma ? 2 : NL * 32 + 1), mbar_init(&s.empty[k], kW + 1);
+        for (int k = 0; k < 2; ++k) mbar_init(&s.posted[k], kW), mbar_init(&s.mail[k], 1), mbar_init(&s.ready[k], 1);
         for (int k = 0; k < kItemSlots; ++k) mbar_init(&s.told[k], 1);
         s.abort = 0;
         fence_mbar_init();
@@ -436,73 +507,25 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, 2)
 
     if (warp > kW) {
         // ------------------------------------------------------------ loading
-        const int w = warp - kW - 1;
-        unsigned int it = 0;
-        for (unsigned int q = 0;; ++q) {
-            const int slot = q % kItemSlots;
-            if (w == 0 && lane == 0) {
-                mbar_arrive_expect_tx(&s.told[slot], 4);
-                if (rank == 0) {
-                    const unsigned int item = counted ? atomicAdd(p.counter, 1u) : blockIdx.x / C + q * (gridDim.x / C);
-                    for (unsigned int k = 0; k < C; ++k) send4(peer_addr(&s.item[slot], k), item, peer_addr(&s.told[slot], k));
+        load_tiles<LOAD>(p, s, warp - kW - 1, lane, rank, C, columns, groups, counted, [&](const int st, const unsigned int g, const unsigned int b, const int round) {
+            const int tile = round * int(C) + int(rank);
+            const int64_t t0 = int64_t(tile) * ROWS;
+            if constexpr (LOAD == kTma) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&s.full[st], sizeof(s.stage[0]));
+                    tma_load_3d(s.stage[st][0], &tm.x, &s.full[st], int(g * 64), int(t0), int(b));
+                    tma_load_3d(s.stage[st][1], &tm.r, &s.full[st], int(g * 64), int(t0), int(b));
+                    tma_load_3d(s.stage[st][2], &tm.i, &s.full[st], int(g * 64), int(t0), int(b));
                 }
+            } else {
+                const int w = warp - kW - 1, steps = int(max(int64_t(0), min(int64_t(ROWS), p.s.L - t0)));
+                const int64_t d = int64_t(g) * 64, width = p.s.D - d;
+                load_rows<T, ROWS, LOAD>(s.stage[st][0], p.x, b * p.xb + t0 * p.xt + d, p.xt, steps, width, pairs, w, lane);
+                load_rows<T, ROWS, LOAD>(s.stage[st][1], p.r, b * p.rb + t0 * p.rt + d, p.rt, steps, width, pairs, w, lane);
+                load_rows<T, ROWS, LOAD>(s.stage[st][2], p.i, b * p.ib + t0 * p.it + d, p.it, steps, width, pairs, w, lane);
             }
-            bool ok = __all_sync(0xffffffffu, wait_phase(&s.told[slot], (q / kItemSlots) & 1, &s.abort, p.status));
-            const unsigned int item = s.item[slot];
-            const bool done = !ok || item >= p.pl.items;
-            const unsigned int seg = done ? 0 : item / columns, col = done ? 0 : item % columns;
-            const int r0 = int(seg) * p.pl.iters, r1 = done ? r0 + 1 : int(min(int64_t(r0 + p.pl.iters), p.pl.rounds));
-            const unsigned int g = col % groups, b = col / groups;
-            for (int round = r0; round < r1; ++round, ++it) {
-                const int st = it % kStages;
-                ok = ok && (it < kStages || wait_phase(&s.empty[st], (it / kStages - 1) & 1, &s.abort, p.status));
-                if (!__all_sync(0xffffffffu, ok)) {  // given up: not before the copies under way have landed
-                    if (LOAD == kTma)
-                        for (unsigned int k = it < kStages ? 0 : it - kStages; k < it; ++k) wait_landed(&s.full[k % kStages], (k / kStages) & 1);
-                    else
-                        asm volatile("cp.async.wait_all;" ::: "memory");
-                    goto out;
-                }
-                const int tile = round * int(C) + int(rank);
-                const int64_t t0 = int64_t(tile) * ROWS;
-                if (w == 0) {
-                    if (lane == 0)
-                        s.tile[it & 3] = {col, seg, done ? -1 : tile, (round == r0 ? 1 : 0) | (round == r1 - 1 ? 2 : 0)};
-                    if (LOAD == kTma && lane == 0) {
-                        if (done) {
-                            mbar_arrive(&s.full[st]);
-                        } else {
-                            mbar_arrive_expect_tx(&s.full[st], sizeof(s.stage[0]));
-                            tma_load_3d(s.stage[st][0], &tm.x, &s.full[st], int(g * 64), int(t0), int(b));
-                            tma_load_3d(s.stage[st][1], &tm.r, &s.full[st], int(g * 64), int(t0), int(b));
-                            tma_load_3d(s.stage[st][2], &tm.i, &s.full[st], int(g * 64), int(t0), int(b));
-                        }
-                    }
-                }
-                if (LOAD != kTma && !done) {
-                    const int steps = int(max(int64_t(0), min(int64_t(ROWS), p.s.L - t0)));
-                    const int64_t d = int64_t(g) * 64, width = p.s.D - d;
-                    load_rows<T, ROWS, LOAD>(s.stage[st][0], p.x + b * p.xb + t0 * p.xt + d, p.xt, steps, width, pairs, w, lane);
-                    load_rows<T, ROWS, LOAD>(s.stage[st][1], p.r + b * p.rb + t0 * p.rt + d, p.rt, steps, width, pairs, w, lane);
-                    load_rows<T, ROWS, LOAD>(s.stage[st][2], p.i + b * p.ib + t0 * p.it + d, p.it, steps, width, pairs, w, lane);
-                }
-                if (w == 0 && !done) {
-#pragma unroll
-                    for (int v = 0; v < 2; ++v) {
-                        const int64_t d = int64_t(g) * 64 + lane * 2 + v;
-                        s.rate[st][lane * 2 + v] = d < p.s.D ? rate(p.lam[d], p.s.c) : 0.0f;
-                    }
-                }
-                __syncwarp();
-                if (w == 0 && lane == 0) mbar_arrive(&s.full[st]);
-                if (LOAD == kAsync) {
-                    copy_async_arrive(&s.full[st]);
-                } else if (LOAD == kPlain) {
-                    mbar_arrive(&s.full[st]);
-                }
-            }
-            if (done) break;
-        }
+            return tile;
+        });
     } else if (warp == kW) {
         // ---------------------------------------------------------- the carry
         float2 S = two(0.0f);
@@ -510,11 +533,27 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, 2)
         for (unsigned int it = 0;; ++it) {
             const bool ok = wait_phase(&s.full[it % kStages], (it / kStages) & 1, &s.abort, p.status);
             if (!__all_sync(0xffffffffu, ok)) break;
-            const TileInfo t = s.tile[it & 3];
+            const TileInfo t = s.tile[it % kInfos];
             if (t.tile < 0) break;
+            __syncwarp();
+            // (a stage is refilled once this warp has seen it too: a phase it misses would look like one to come)
+            if (lane == 0) mbar_arrive(&s.empty[it % kStages]);
             const int64_t d = int64_t(t.col % groups) * 64 + lane * 2, o = int64_t(t.col / groups) * p.s.D + d;
             const int have = int(min(int64_t(2), p.s.D - d));  // channels of this lane (at most 2)
-            if (lane == 0) mbar_arrive_expect_tx(&s.mail[it & 1], C * sizeof(s.inbox[0][0]));
+            const int buf = it & 1;
+            const uint32_t phase = (it >> 1) & 1;
+            if (lane == 0 && C > 1) mbar_arrive_expect_tx(&s.mail[buf], C * sizeof(s.inbox[0][0]));
+            wait_phase(&s.posted[buf], phase, &s.abort, p.status);
+            float4 m[kW];
+#pragma unroll
+            for (int w = 0; w < kW; ++w) m[w] = s.maps[buf][w][lane];
+            float4 f[kW / 2];
+#pragma unroll
+            for (int w = 0; w < kW / 2; ++w) f[w] = then2(m[2 * w], m[2 * w + 1]);
+            const float4 own = then2(then2(f[0], f[1]), then2(f[2], f[3]));
+            if (C > 1)
+                for (unsigned int k = 0; k < C; ++k)
+                    send16(peer_addr(&s.inbox[buf][rank][lane], k), own, peer_addr(&s.mail[buf], k));
             if (t.flags & 1) {
                 S = two(0.0f);
                 M = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
@@ -529,17 +568,26 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, 2)
                     }
                 }
             }
-            wait_phase(&s.mail[it & 1], (it >> 1) & 1, &s.abort, p.status);
             float2 mine = S;
-            for (unsigned int k = 0; k < C; ++k) {
-                const float4 m = s.inbox[it & 1][k][lane];
-                if (k == rank) mine = S;
-                S = apply2(m, S);
-                if (p.maps) M = then2(M, m);
+            if (C > 1) {
+                wait_phase(&s.mail[buf], phase, &s.abort, p.status);
+                for (unsigned int k = 0; k < C; ++k) {
+                    const float4 g = s.inbox[buf][k][lane];
+                    if (k == rank) mine = S;
+                    S = apply2(g, S);
+                    if (p.maps) M = then2(M, g);
+                }
+            } else {
+                S = apply2(own, S);
+                if (p.maps) M = then2(M, own);
             }
-            *reinterpret_cast<float2 *>(&s.start[it & 1][lane * 2]) = mine;
+#pragma unroll
+            for (int w = 0; w < kW; ++w) {
+                *reinterpret_cast<float2 *>(&s.maps[buf][w][lane]) = mine;
+                mine = apply2(m[w], mine);
+            }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s.ready[it & 1]);
+            if (lane == 0) mbar_arrive(&s.ready[buf]);
             if ((t.flags & 2) && rank == 0) {
                 if (p.maps) {
                     if (have > 0) p.maps[int64_t(t.seg) * n + o] = Map{M.x, M.y};
@@ -554,15 +602,11 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, 2)
     } else {
         // ---------------------------------------------------------- computing
         for (unsigned int it = 0;; ++it) {
-            const int st = it % kStages;
+            const int st = it % kStages, buf = it & 1;
             const bool ok = wait_phase(&s.full[st], (it / kStages) & 1, &s.abort, p.status);
-            TileInfo t{};
-            t.tile = -1;
-            if (__all_sync(0xffffffffu, ok)) t = s.tile[it & 3];
-            if (t.tile < 0) {  // the end, or a wait that gave up: the computing warps leave together
-                compute_sync(false);
-                break;
-            }
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const TileInfo t = s.tile[it % kInfos];
+            if (t.tile < 0) break;
             const unsigned int b = t.col / groups;
             const int64_t d = int64_t(t.col % groups) * 64 + lane * 2, o = int64_t(b) * p.s.D + d;
             const int64_t t0 = int64_t(t.tile) * ROWS + warp * K;
@@ -575,54 +619,51 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, 2)
             float2 a[K], h[K];
             float4 m;
             float big = 1e30f;
-            if (__all_sync(0xffffffffu, fmaxf(rt.x, rt.y) < 0.5f)) m = fwd_steps_of<T, K, true>(x, r, i, rt, fresh, a, h, big);
+            if (fresh == 0 && __all_sync(0xffffffffu, fmaxf(rt.x, rt.y) < 0.5f && fminf(rt.x, rt.y) > 1e-18f)) m = fwd_steps_of<T, K, true>(x, r, i, rt, fresh, a, h, big);
             if (__any_sync(0xffffffffu, big > 60.0f)) m = fwd_steps_of<T, K, false>(x, r, i, rt, fresh, a, h, big);
-            if (warp < kW - 1) s.maps[it & 1][warp][lane] = m;
-            if (!compute_sync(true)) break;
-            if (threadIdx.x == 0) mbar_arrive(&s.empty[st]);
-            if (warp == kW - 1) {
-                float4 all = s.maps[it & 1][0][lane];
-#pragma unroll
-                for (int w = 1; w < kW - 1; ++w) all = then2(all, s.maps[it & 1][w][lane]);
-                all = then2(all, m);
-                for (unsigned int k = 0; k < C; ++k)
-                    send16(peer_addr(&s.inbox[it & 1][rank][lane], k), all, peer_addr(&s.mail[it & 1], k));
+            s.maps[buf][warp][lane] = m;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&s.posted[buf]);
+                mbar_arrive(&s.empty[st]);
             }
-            wait_phase(&s.ready[it & 1], (it >> 1) & 1, &s.abort, p.status);
-            if (p.maps || d >= p.s.D || steps == 0) continue;
-            float2 hs = *reinterpret_cast<const float2 *>(&s.start[it & 1][lane * 2]);
-            for (int w = 0; w < warp; ++w) hs = apply2(s.maps[it & 1][w][lane], hs);
-            const bool both = d + 1 < p.s.D;
-            if (p.states && t0 % kChunk == 0) {
-                float *q = p.states + (int64_t(b) * ((p.s.L + kChunk - 1) / kChunk) + t0 / kChunk) * p.s.D + d;
-                q[0] = hs.x;
-                if (both) q[1] = hs.y;
-            }
-            T *yp = p.y + (int64_t(b) * p.s.L + t0) * p.s.D + d;
-            if (steps == K && p.y && pairs) {
-#pragma unroll
-                for (int k = 0; k < K; ++k, yp += p.s.D) {
-                    hs = (fresh >> k & 1) ? h[k] : fma2(a[k], hs, h[k]);
-                    store2(yp, hs);
+            wait_phase(&s.ready[buf], (it >> 1) & 1, &s.abort, p.status);
+            if (!p.maps && d < p.s.D && steps > 0) {
+                float2 hs = *reinterpret_cast<const float2 *>(&s.maps[buf][warp][lane]);
+                const bool both = d + 1 < p.s.D;
+                if (p.states && t0 % kChunk == 0) {
+                    float *q = p.states + (int64_t(b) * ((p.s.L + kChunk - 1) / kChunk) + t0 / kChunk) * p.s.D + d;
+                    q[0] = hs.x;
+                    if (both) q[1] = hs.y;
                 }
-            } else {
+                T *yp = p.y + (int64_t(b) * p.s.L + t0) * p.s.D + d;
+                if (steps == K && fresh == 0 && p.y && pairs) {
 #pragma unroll
-                for (int k = 0; k < K; ++k, yp += p.s.D)
-                    if (k < steps) {
-                        hs = (fresh >> k & 1) ? h[k] : fma2(a[k], hs, h[k]);
-                        if (p.y) {
-                            yp[0] = Tok<T>::from_f(hs.x);
-                            if (both) yp[1] = Tok<T>::from_f(hs.y);
-                        }
+                    for (int k = 0; k < K; ++k, yp += p.s.D) {
+                        hs = fma2(a[k], hs, h[k]);
+                        store2(yp, hs);
                     }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < K; ++k, yp += p.s.D)
+                        if (k < steps) {
+                            hs = (fresh >> k & 1) ? h[k] : fma2(a[k], hs, h[k]);
+                            if (p.y && pairs) {
+                                store2(yp, hs);
+                            } else if (p.y) {
+                                yp[0] = Tok<T>::from_f(hs.x);
+                                if (both) yp[1] = Tok<T>::from_f(hs.y);
+                            }
+                        }
+                }
+                if (p.h_last && t0 + steps == p.s.L) {
+                    p.h_last[o] = hs.x;
+                    if (both) p.h_last[o + 1] = hs.y;
+                }
             }
-            if (p.h_last && t0 + steps == p.s.L) {
-                p.h_last[o] = hs.x;
-                if (both) p.h_last[o + 1] = hs.y;
-            }
+            __syncwarp();
         }
     }
-out:
     __syncwarp();
     cluster_sync_all();  // no block leaves while another may still write to it
 }
@@ -640,186 +681,360 @@ __global__ void __launch_bounds__(128)
     }
 }
 
-// Chains the tiles' maps of every channel: starts[j] is the state entering tile j; for the
-// backward (from the last tile to the first) the adjoint entering it from its right end.
-__global__ void gated_chain_kernel(int64_t n, int64_t tiles, bool backward, const float *__restrict__ first,
-                                   const Map *__restrict__ maps, float *__restrict__ starts) {
-    const int64_t k = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (k >= n) return;
-    float h = first ? first[k] : 0.0f;
-#pragma unroll 8
-    for (int64_t j = 0; j < tiles; ++j) {
-        const int64_t o = (backward ? tiles - 1 - j : j) * n + k;
-        const Map m = maps[o];
-        starts[o] = h;
-        h = apply(m, h);
-    }
-    if (backward) starts[tiles * n + k] = h;
-}
-
 // ------------------------------------------------------------------ backward
 template <typename T>
 struct BwdArgs {
     Shape s;
+    Plan pl;
+    unsigned int *counter, *status;
+    unsigned long long *starts;  // [segs][B D] adjoints entering the segments from their right
+    Map *maps;                   // [segs][B D] the segments' maps (local pass)
     const T *x, *r, *i, *dy;
     int64_t xb, xt, rb, rt, ib, it;
     const uint8_t *reset;
-    const float *lam, *states;
+    const float *lam, *states, *dh_last;
     T *dx, *dr, *di;
-    float *dh0, *starts, *parts;
-    Map *maps;
+    float *dh0, *parts;          // parts: [segs][cluster][warps][B][D] sums of dw sigmoid(r)
 };
 
-// v_t = dL/dh_t follows v_t = dy_t + a_{t+1} v_{t+1}; with g_t = a_t v_t, what a step hands
-// to the one before it, a piece of time acts on the g entering from its right as
-// g -> P g + G with the forward's P.
-template <typename T, int V, bool MAIN>
-__global__ void __launch_bounds__(kW * 32) gated_bwd_kernel(const BwdArgs<T> p) {
-    constexpr int K = kKB;
-    __shared__ Map sf[kW][V][32], sb[kW][V][32];
-    __shared__ float sl[kW][V][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t g = blockIdx.x % p.s.groups, jb = blockIdx.x / p.s.groups;
-    const int64_t b = jb % p.s.B, j = jb / p.s.B;
-    const int64_t d = (g * 32 + lane) * V;
-    const int64_t t0 = (j * kW + warp) * K;
-    const bool on = d < p.s.D;
-    const int n = int(max(int64_t(0), min(int64_t(K), p.s.L - t0)));
+template <typename T, int K>
+struct BwdShared {
+    static constexpr int kMaxCluster = 8;
+    T stage[kStages][4][kW * K][64];  // x, r, i, dy of a tile; then dx, dr, di in the first three
+    float4 maps[2][kW][32];           // a warp's map of the state, then its start: h and g of a lane's two channels
+    float2 adj[2][kW][32];            // H of its map of the adjoint (P is the same)
+    float4 inbox[2][kMaxCluster][32];
+    float rate[kStages][64];
+    TileInfo tile[kInfos];
+    uint64_t full[kStages], empty[kStages], posted[2], mail[2], ready[2], told[kItemSlots];
+    unsigned int item[kItemSlots];
+    int abort;
+};
 
-    float rt[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) rt[v] = on ? rate(p.lam[d + v], p.s.c) : 0.0f;
-    Vec<T, V> xv[K], rv[K], iv[K], dv[K];
-    const T *xp = p.x + b * p.xb + t0 * p.xt + d, *rp = p.r + b * p.rb + t0 * p.rt + d,
-            *ip = p.i + b * p.ib + t0 * p.it + d, *dp = p.dy + (b * p.s.L + t0) * p.s.D + d;
+struct Maps7 {
+    CUtensorMap x, r, i, dy, dx, dr, di;
+};
+
+// v_t = dL/dh_t follows v_t = dy_t + a_{t+1} v_{t+1}; with g_t = a_t v_t, what a step hands to
+// the one before it, a piece of time acts on the g entering from its right as g -> P g + G
+// with the forward's P. Steps past the end are the identity.
+template <typename T, int K, bool FAST>
+__device__ __forceinline__ void bwd_steps_of(const T *x, const T *r, const T *i, const T *dy, const float2 rt, const unsigned int fresh,
+                                             const int steps, float2 (&a)[K], float2 (&h)[K], float2 (&sr)[K], float2 (&si)[K],
+                                             float4 &f, float2 &g, float &big) {
+    float2 P = two(1.0f), H = two(0.0f), G = two(0.0f);
+    float top = -1.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        if (on && k < n) {
-            xv[k] = ldv<T, V>(xp + k * p.xt);
-            rv[k] = ldv<T, V>(rp + k * p.rt);
-            iv[k] = ldv<T, V>(ip + k * p.it);
-            dv[k] = ldv<T, V>(dp + k * p.s.D);
+        float2 e;
+        if constexpr (FAST) {
+            const float2 tr = mul2(load2(r + k * 64), two(-kLog2e)), ti = mul2(load2(i + k * 64), two(-kLog2e));
+            top = fmaxf(fmaxf(top, fmaxf(tr.x, tr.y)), fmaxf(ti.x, ti.y));
+            const float2 fr = add2(two(1.0f), make_float2(ex2_approx(tr.x), ex2_approx(tr.y)));
+            const float2 fi = add2(two(1.0f), make_float2(ex2_approx(ti.x), ex2_approx(ti.y)));
+            const float2 pr = mul2(fr, fi), rc = make_float2(rcp_approx(pr.x), rcp_approx(pr.y));
+            sr[k] = mul2(rc, fi);
+            si[k] = mul2(rc, fr);
         } else {
-            for (int v = 0; v < V; ++v) xv[k].set(v, 0.0f), rv[k].set(v, 0.0f), iv[k].set(v, 0.0f), dv[k].set(v, 0.0f);
+            sr[k] = sigmoid2(load2(r + k * 64));
+            si[k] = sigmoid2(load2(i + k * 64));
+        }
+        a[k] = decay2<FAST>(mul2(rt, sr[k]), e);
+        const float2 sq = mul2(e, fma2(e, two(-1.0f), two(2.0f)));
+        const float2 u = mul2(si[k], load2(x + k * 64));
+        if constexpr (FAST) {
+            h[k] = mul2(mul2(sq, make_float2(rsqrt_approx(sq.x), rsqrt_approx(sq.y))), u);
+            P = mul2(P, a[k]);
+            H = fma2(a[k], H, h[k]);
+        } else {
+            const bool fr = fresh >> k & 1;
+            h[k] = fr ? u : mul2(make_float2(sqrt_approx(sq.x), sqrt_approx(sq.y)), u);
+            if (k >= steps) a[k] = two(1.0f);
+            P = mul2(P, a[k]);
+            H = fr ? h[k] : fma2(a[k], H, h[k]);
         }
     }
-    unsigned fresh = 0;
-    if (p.reset)
-        for (int k = 0; k < K; ++k)
-            if (k < n && p.reset[b * p.s.L + t0 + k]) fresh |= 1u << k;
-
-    float a[K][V], h[K][V];  // the decay, and the input; then the state before the step
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float e;
-            const float dec = decay(rt[v] * sigmoid_f(rv[k].get(v)), e);
-            const float sq = e * (2.0f - e), u = sigmoid_f(iv[k].get(v)) * xv[k].get(v);
-            a[k][v] = k < n ? dec : 1.0f;
-            h[k][v] = (fresh >> k & 1) ? u : sq * inv_beta(sq) * u;
-        }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        Map f{1.0f, 0.0f}, r{1.0f, 0.0f};
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            f.P *= a[k][v];
-            f.H = (fresh >> k & 1) ? h[k][v] : fmaf(a[k][v], f.H, h[k][v]);
-        }
-#pragma unroll
-        for (int k = K - 1; k >= 0; --k) r.H = (fresh >> k & 1) ? 0.0f : a[k][v] * (dv[k].get(v) + r.H);
-        f.P = r.P = fresh ? 0.0f : keep(f.P);
-        sf[warp][v][lane] = f;
-        sb[warp][v][lane] = r;
-    }
-    __syncthreads();
-    if (!MAIN) {
-        if (warp == 0 && on) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                Map m = sb[kW - 1][v][lane];
-                for (int w = kW - 2; w >= 0; --w) m = then(m, sb[w][v][lane]);
-                p.maps[(j * p.s.B + b) * p.s.D + d + v] = m;
-            }
-        }
-        return;
-    }
-    float gr[V], dl[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float hs = on ? p.states[(b * p.s.tiles + j) * p.s.D + d + v] : 0.0f;
-        for (int w = 0; w < warp; ++w) hs = apply(sf[w][v][lane], hs);
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const float next = (fresh >> k & 1) ? h[k][v] : fmaf(a[k][v], hs, h[k][v]);
-            h[k][v] = hs;
-            hs = next;
-        }
-        gr[v] = on ? p.starts[(j * p.s.B + b) * p.s.D + d + v] : 0.0f;
-        for (int w = kW - 1; w > warp; --w) gr[v] = apply(sb[w][v][lane], gr[v]);
-        dl[v] = 0.0f;
-    }
-    T *dxp = p.dx + (b * p.s.L + t0) * p.s.D + d, *drp = p.dr + (b * p.s.L + t0) * p.s.D + d,
-      *dip = p.di + (b * p.s.L + t0) * p.s.D + d;
 #pragma unroll
     for (int k = K - 1; k >= 0; --k) {
-        if (k < n) {
-            const bool fr = fresh >> k & 1;
-            Vec<T, V> ox, orr, oi;
+        if (FAST || k < steps) G = (!FAST && (fresh >> k & 1)) ? two(0.0f) : mul2(a[k], add2(load2(dy + k * 64), G));
+    }
+    big = top;
+    f = make_float4(fresh ? 0.0f : keep(P.x), H.x, fresh ? 0.0f : keep(P.y), H.y);
+    g = G;
+}
+
+// The gradients of a thread's steps, from the state entering them on the left and the adjoint on the right, given
+// to out(k, dx, dr, di) from the last step to the first; the sum of dw sigmoid(r).
+template <typename T, int K, bool FAST, typename Out>
+__device__ __forceinline__ float2 bwd_grads_of(const T *x, const T *dy, const float2 rt, const unsigned int fresh, const int steps,
+                                               const float2 (&a)[K], float2 (&h)[K], const float2 (&sr)[K], const float2 (&si)[K],
+                                               float2 hs, float2 gs, const Out &out) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float sr = sigmoid_f(rv[k].get(v)), si = sigmoid_f(iv[k].get(v));
-                const float w = rt[v] * sr, at = a[k][v], e = w < 0.5f ? small_e(w) : 1.0f - at;
-                const float sq = e * (2.0f - e), q = inv_beta(sq);
-                const float u = si * xv[k].get(v), vt = dv[k].get(v) + gr[v];
-                const float vb = fr ? vt : vt * sq * q;
-                // dL/dw = a v (a u / beta - h_{t-1}); beta -> 0 only as w -> 0, where w / beta -> 0
-                const float dw = fr ? 0.0f : at * vt * fmaf(at * q, u, -h[k][v]);
-                ox.set(v, vb * si);
-                oi.set(v, vb * u * (1.0f - si));
-                orr.set(v, dw * w * (1.0f - sr));
-                dl[v] = fmaf(dw, sr, dl[v]);
-                gr[v] = fr ? 0.0f : at * vt;
+    for (int k = 0; k < K; ++k) {  // h[k]: the state before the step
+        const float2 next = (!FAST && (fresh >> k & 1)) ? h[k] : fma2(a[k], hs, h[k]);
+        h[k] = hs;
+        hs = next;
+    }
+    float2 dl = two(0.0f);
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+        if (!FAST && k >= steps) continue;
+        const bool fr = !FAST && (fresh >> k & 1);
+        const float2 v = add2(load2(dy + k * 64), gs), w = mul2(rt, sr[k]), u = mul2(si[k], load2(x + k * 64));
+        float2 e = small_e2(w);
+        if (!FAST) e = make_float2(w.x < 0.5f ? e.x : 1.0f - a[k].x, w.y < 0.5f ? e.y : 1.0f - a[k].y);
+        const float2 sq = mul2(e, fma2(e, two(-1.0f), two(2.0f)));
+        const float2 q = FAST ? make_float2(rsqrt_approx(sq.x), rsqrt_approx(sq.y)) : make_float2(inv_beta(sq.x), inv_beta(sq.y));
+        const float2 vb = fr ? v : mul2(v, mul2(sq, q)), av = mul2(a[k], v);
+        // dL/dw = a v (a u / beta - h_{t-1}); beta -> 0 only as w -> 0, where w / beta -> 0
+        float2 dw = mul2(av, fma2(mul2(a[k], q), u, mul2(h[k], two(-1.0f))));
+        if (fr) dw = two(0.0f);
+        const float2 ws = mul2(w, fma2(sr[k], two(-1.0f), two(1.0f))), vu = mul2(vb, u);
+        out(k, mul2(vb, si[k]), mul2(dw, ws), mul2(vu, fma2(si[k], two(-1.0f), two(1.0f))));
+        dl = fma2(dw, sr[k], dl);
+        gs = fr ? two(0.0f) : av;
+    }
+    return dl;
+}
+
+// The forward's scheme from the end of time to its beginning: a tile is a chunk, whose state
+// is known, so only the adjoint passes from block to block. The decays, inputs and sigmoids of a thread's
+// steps stay in registers between the two passes over them; a tile's tokens stay in
+// its stage until its gradients, written over them, have left.
+template <typename T, int K, Load LOAD>
+__global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, sizeof(T) == 2 ? 2 : 1)
+    gated_bwd_kernel(const BwdArgs<T> p, const __grid_constant__ Maps7 tm, const bool pairs) {
+    constexpr int NL = kLoaders<LOAD>, ROWS = kW * K;
+    static_assert(ROWS == kChunk, "a tile is a chunk");
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    BwdShared<T, K> &s = *reinterpret_cast<BwdShared<T, K> *>(smem_raw);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned int groups = unsigned(p.s.groups), columns = unsigned(p.pl.columns), C = unsigned(p.pl.cluster);
+    const uint32_t rank = cluster_rank();
+    const bool counted = p.pl.segs > 1 && !p.pl.local;
+    const int64_t n = p.s.B * p.s.D, chunks = (p.s.L + kChunk - 1) / kChunk;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < kStages; ++k) mbar_init(&s.full[k], LOAD == kTma ? 2 : NL * 32 + 1), mbar_init(&s.empty[k], kW + 1);
+        for (int k = 0; k < 2; ++k) mbar_init(&s.posted[k], kW), mbar_init(&s.mail[k], 1), mbar_init(&s.ready[k], 1);
+        for (int k = 0; k < kItemSlots; ++k) mbar_init(&s.told[k], 1);
+        s.abort = 0;
+        fence_mbar_init();
+        if (blockIdx.x == 0 && (p.pl.segs == 1 || p.maps)) *p.status = 0;  // (else cleared with the states)
+    }
+    cluster_sync_all();
+
+    if (warp > kW) {
+        // ------------------------------------------------------------ loading
+        load_tiles<LOAD>(p, s, warp - kW - 1, lane, rank, C, columns, groups, counted, [&](const int st, const unsigned int g, const unsigned int b, const int round) {
+            const int tile = int(p.pl.rounds * C) - 1 - (round * int(C) + int(rank));
+            const int64_t t0 = int64_t(tile) * ROWS;
+            if constexpr (LOAD == kTma) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&s.full[st], sizeof(s.stage[0]));
+                    tma_load_3d(s.stage[st][0], &tm.x, &s.full[st], int(g * 64), int(t0), int(b));
+                    tma_load_3d(s.stage[st][1], &tm.r, &s.full[st], int(g * 64), int(t0), int(b));
+                    tma_load_3d(s.stage[st][2], &tm.i, &s.full[st], int(g * 64), int(t0), int(b));
+                    tma_load_3d(s.stage[st][3], &tm.dy, &s.full[st], int(g * 64), int(t0), int(b));
+                }
+            } else {
+                const int w = warp - kW - 1, steps = int(max(int64_t(0), min(int64_t(ROWS), p.s.L - t0)));
+                const int64_t d = int64_t(g) * 64, width = p.s.D - d;
+                load_rows<T, ROWS, LOAD>(s.stage[st][0], p.x, b * p.xb + t0 * p.xt + d, p.xt, steps, width, pairs, w, lane);
+                load_rows<T, ROWS, LOAD>(s.stage[st][1], p.r, b * p.rb + t0 * p.rt + d, p.rt, steps, width, pairs, w, lane);
+                load_rows<T, ROWS, LOAD>(s.stage[st][2], p.i, b * p.ib + t0 * p.it + d, p.it, steps, width, pairs, w, lane);
+                load_rows<T, ROWS, LOAD>(s.stage[st][3], p.dy, (int64_t(b) * p.s.L + t0) * p.s.D + d, p.s.D, steps, width, pairs, w, lane);
             }
-            if (on) {
-                stv<T, V>(dxp + k * p.s.D, ox);
-                stv<T, V>(drp + k * p.s.D, orr);
-                stv<T, V>(dip + k * p.s.D, oi);
+            return tile;
+        });
+    } else if (warp == kW) {
+        // ---------------------------------------------------------- the carry
+        float2 S = two(0.0f);
+        float4 M = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+        for (unsigned int it = 0;; ++it) {
+            const bool ok = wait_phase(&s.full[it % kStages], (it / kStages) & 1, &s.abort, p.status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const TileInfo t = s.tile[it % kInfos];
+            if (t.tile < 0) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.empty[it % kStages]);
+            const unsigned int b = t.col / groups;
+            const int64_t d = int64_t(t.col % groups) * 64 + lane * 2, o = int64_t(b) * p.s.D + d;
+            const int have = int(min(int64_t(2), p.s.D - d));  // channels of this lane (at most 2)
+            const int buf = it & 1;
+            const uint32_t phase = (it >> 1) & 1;
+            if (lane == 0 && C > 1) mbar_arrive_expect_tx(&s.mail[buf], C * sizeof(s.inbox[0][0]));
+            float2 hs = two(0.0f);
+            if (t.tile < chunks && !p.maps) {
+                const float *q = p.states + (int64_t(b) * chunks + t.tile) * p.s.D + d;
+                if (have > 0) hs.x = q[0];
+                if (have > 1) hs.y = q[1];
+            }
+            wait_phase(&s.posted[buf], phase, &s.abort, p.status);
+            float4 m[kW], r[kW];  // the state's maps, and the adjoint's from the last warp to the first
+#pragma unroll
+            for (int w = 0; w < kW; ++w) {
+                m[w] = s.maps[buf][w][lane];
+                const float2 g = s.adj[buf][w][lane];
+                r[kW - 1 - w] = make_float4(m[w].x, g.x, m[w].z, g.y);
+            }
+            const float4 own = then2(then2(then2(r[0], r[1]), then2(r[2], r[3])), then2(then2(r[4], r[5]), then2(r[6], r[7])));
+            if (C > 1)
+                for (unsigned int k = 0; k < C; ++k)
+                    send16(peer_addr(&s.inbox[buf][rank][lane], k), own, peer_addr(&s.mail[buf], k));
+            if (t.flags & 1) {
+                S = two(0.0f);
+                M = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
+                if (!p.maps) {
+                    const unsigned long long *q = p.starts + int64_t(t.seg) * n + o;
+                    if (t.seg == 0) {
+                        if (p.dh_last && have > 0) S.x = p.dh_last[o];
+                        if (p.dh_last && have > 1) S.y = p.dh_last[o + 1];
+                    } else {
+                        if (have > 0) S.x = __uint_as_float(unsigned(wait_word(q, p.status)));
+                        if (have > 1) S.y = __uint_as_float(unsigned(wait_word(q + 1, p.status)));
+                    }
+                }
+            }
+            float2 mine = S;
+            if (C > 1) {
+                wait_phase(&s.mail[buf], phase, &s.abort, p.status);
+                for (unsigned int k = 0; k < C; ++k) {
+                    const float4 g = s.inbox[buf][k][lane];
+                    if (k == rank) mine = S;
+                    S = apply2(g, S);
+                    if (p.maps) M = then2(M, g);
+                }
+            } else {
+                S = apply2(own, S);
+                if (p.maps) M = then2(M, own);
+            }
+            float2 gs[kW];
+#pragma unroll
+            for (int w = 0; w < kW; ++w) {
+                gs[kW - 1 - w] = mine;
+                mine = apply2(r[w], mine);
+            }
+#pragma unroll
+            for (int w = 0; w < kW; ++w) {
+                s.maps[buf][w][lane] = make_float4(hs.x, hs.y, gs[w].x, gs[w].y);
+                hs = apply2(m[w], hs);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.ready[buf]);
+            if ((t.flags & 2) && rank == 0) {
+                if (p.maps) {
+                    if (have > 0) p.maps[int64_t(t.seg) * n + o] = Map{M.x, M.y};
+                    if (have > 1) p.maps[int64_t(t.seg) * n + o + 1] = Map{M.z, M.w};
+                } else if (int(t.seg) + 1 == p.pl.segs) {
+                    if (p.dh0 && have > 0) p.dh0[o] = S.x;
+                    if (p.dh0 && have > 1) p.dh0[o + 1] = S.y;
+                } else if (counted) {
+                    unsigned long long *q = p.starts + int64_t(t.seg + 1) * n + o;
+                    if (have > 0) st_word(q, pack(S.x));
+                    if (have > 1) st_word(q + 1, pack(S.y));
+                }
             }
         }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        sl[warp][v][lane] = dl[v];
-        if (p.dh0 && t0 == 0 && on) p.dh0[b * p.s.D + d + v] = gr[v];
-    }
-    __syncthreads();
-    if (warp == 0 && on) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float t = 0.0f;
-            for (int w = 0; w < kW; ++w) t += sl[w][v][lane];
-            p.parts[(j * p.s.B + b) * p.s.D + d + v] = t;
+    } else {
+        // ---------------------------------------------------------- computing
+        float2 dl = two(0.0f);
+        for (unsigned int it = 0;; ++it) {
+            const int st = it % kStages, buf = it & 1;
+            const bool ok = wait_phase(&s.full[st], (it / kStages) & 1, &s.abort, p.status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const TileInfo t = s.tile[it % kInfos];
+            if (t.tile < 0) break;
+            const unsigned int b = t.col / groups;
+            const int64_t d = int64_t(t.col % groups) * 64 + lane * 2;
+            const int64_t t0 = int64_t(t.tile) * ROWS + warp * K;
+            const int steps = int(max(int64_t(0), min(int64_t(K), p.s.L - t0)));
+            unsigned int fresh = 0;
+            if (p.reset) fresh = __ballot_sync(0xffffffffu, lane < steps && p.reset[int64_t(b) * p.s.L + t0 + lane] != 0);
+            const float2 rt = *reinterpret_cast<const float2 *>(&s.rate[st][lane * 2]);
+            T *x = &s.stage[st][0][warp * K][lane * 2], *r = &s.stage[st][1][warp * K][lane * 2], *i = &s.stage[st][2][warp * K][lane * 2];
+            const T *dy = &s.stage[st][3][warp * K][lane * 2];
+            float2 a[K], h[K], sr[K], si[K], g;
+            float4 m;
+            float big = 1e30f;
+            if (fresh == 0 && steps == K && __all_sync(0xffffffffu, fmaxf(rt.x, rt.y) < 0.5f && fminf(rt.x, rt.y) > 1e-18f))
+                bwd_steps_of<T, K, true>(x, r, i, dy, rt, fresh, steps, a, h, sr, si, m, g, big);
+            const bool slow = __any_sync(0xffffffffu, big > 60.0f);
+            if (slow) bwd_steps_of<T, K, false>(x, r, i, dy, rt, fresh, steps, a, h, sr, si, m, g, big);
+            s.maps[buf][warp][lane] = m;
+            s.adj[buf][warp][lane] = g;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.posted[buf]);
+            if (LOAD == kTma && it > 0 && lane == 0) {  // the last tile's gradients have left its stage
+                bulk_wait_read<0>();
+                mbar_arrive(&s.empty[(it - 1) % kStages]);
+            }
+            wait_phase(&s.ready[buf], (it >> 1) & 1, &s.abort, p.status);
+            if (!p.maps) {
+                const float4 begin = s.maps[buf][warp][lane];
+                const float2 hs = make_float2(begin.x, begin.y), gs = make_float2(begin.z, begin.w);
+                if (t.flags & 1) dl = two(0.0f);
+                if constexpr (LOAD == kTma) {
+                    const auto out = [&](const int k, const float2 gx, const float2 gr, const float2 gi) {
+                        store2(x + k * 64, gx);
+                        store2(r + k * 64, gr);
+                        store2(i + k * 64, gi);
+                    };
+                    dl = add2(dl, slow ? bwd_grads_of<T, K, false>(x, dy, rt, fresh, steps, a, h, sr, si, hs, gs, out)
+                                       : bwd_grads_of<T, K, true>(x, dy, rt, fresh, steps, a, h, sr, si, hs, gs, out));
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && steps > 0) {
+                        tma_store_3d(&tm.dx, x, int(d), int(t0), int(b));
+                        tma_store_3d(&tm.dr, r, int(d), int(t0), int(b));
+                        tma_store_3d(&tm.di, i, int(d), int(t0), int(b));
+                    }
+                    if (lane == 0) bulk_commit();
+                } else {
+                    const int64_t o = (int64_t(b) * p.s.L + t0) * p.s.D + d;
+                    const bool on = d < p.s.D, both = d + 1 < p.s.D;
+                    const auto out = [&](const int k, const float2 gx, const float2 gr, const float2 gi) {
+                        const int64_t q = o + k * p.s.D;
+                        if (pairs) {
+                            if (on) store2(p.dx + q, gx), store2(p.dr + q, gr), store2(p.di + q, gi);
+                        } else {
+                            if (on) p.dx[q] = Tok<T>::from_f(gx.x), p.dr[q] = Tok<T>::from_f(gr.x), p.di[q] = Tok<T>::from_f(gi.x);
+                            if (both) p.dx[q + 1] = Tok<T>::from_f(gx.y), p.dr[q + 1] = Tok<T>::from_f(gr.y), p.di[q + 1] = Tok<T>::from_f(gi.y);
+                        }
+                    };
+                    dl = add2(dl, slow ? bwd_grads_of<T, K, false>(x, dy, rt, fresh, steps, a, h, sr, si, hs, gs, out)
+                                       : bwd_grads_of<T, K, true>(x, dy, rt, fresh, steps, a, h, sr, si, hs, gs, out));
+                }
+                if (t.flags & 2) {
+                    float *q = p.parts + (((int64_t(t.seg) * C + rank) * kW + warp) * p.s.B + b) * p.s.D + d;
+                    if (d < p.s.D) q[0] = dl.x;
+                    if (d + 1 < p.s.D) q[1] = dl.y;
+                }
+            }
+            __syncwarp();
+            if (LOAD != kTma && lane == 0) mbar_arrive(&s.empty[st]);
         }
+        if (LOAD == kTma && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
+    __syncwarp();
+    cluster_sync_all();  // no block leaves while another may still write to it
 }
 
 // dlam[d] = c sigmoid(lam[d]) * the sum of the tiles' parts, in a fixed order.
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
     gated_dlam_kernel(int64_t rows, int64_t D, float c, const float *__restrict__ parts, const float *__restrict__ lam,
                       float *__restrict__ dlam) {
-    __shared__ float s[8][32];
+    __shared__ float s[32][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t d = int64_t(blockIdx.x) * 32 + lane;
     float t = 0.0f;
     if (d < D)
-        for (int64_t k = warp; k < rows; k += 8) t += parts[k * D + d];
+#pragma unroll 4
+        for (int64_t k = warp; k < rows; k += 32) t += parts[k * D + d];
     s[warp][lane] = t;
     __syncthreads();
     if (warp == 0 && d < D) {
         t = 0.0f;
-        for (int w = 0; w < 8; ++w) t += s[w][lane];
+        for (int w = 0; w < 32; ++w) t += s[w][lane];
         dlam[d] = t * c / (1.0f + expf(-lam[d]));
     }
 }
@@ -872,6 +1087,9 @@ ssm_status launched() { return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_
 // Segments a column's time may be cut into: enough to deal the columns out evenly.
 int max_segs(int64_t columns, int64_t chunks) { return int(std::max<int64_t>(1, std::min<int64_t>(chunks, std::max<int64_t>(8, std::min<int64_t>(256, 4096 / columns))))); }
 
+// Segments times blocks of a cluster: what each column's sums of dlam are spread over at most.
+int most_parts(int64_t columns) { return int(std::max<int64_t>(16, std::min<int64_t>(256, 4096 / columns))); }
+
 size_t carry_bytes(int64_t B, int64_t L, int64_t D) {
     const int64_t segs = max_segs(B * ceil_div(D, 64), ceil_div(L, kChunk));
     return kWsHeader + 2 * up256(size_t(B) * size_t(D) * size_t(segs) * 8);
@@ -879,7 +1097,7 @@ size_t carry_bytes(int64_t B, int64_t L, int64_t D) {
 
 // Clusters of each size that the GPU holds at once (0: not asked yet), by device.
 struct Residency {
-    std::atomic<int> n[64][4];
+    std::atomic<int> n[64][5];
 };
 int clusters_resident(Residency &r, const void *kernel, int threads, size_t smem, int log2c) {
     int dev = 0;
@@ -893,6 +1111,7 @@ int clusters_resident(Residency &r, const void *kernel, int threads, size_t smem
         at.val.clusterDim.x = 1u << log2c, at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
         cfg.attrs = &at, cfg.numAttrs = 1;
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess ||
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
             cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0)
             return 0;
         r.n[dev][log2c].store(n, std::memory_order_relaxed);
@@ -905,10 +1124,11 @@ int clusters_resident(Residency &r, const void *kernel, int threads, size_t smem
 // in as many pieces as even out the last turn; with fewer, larger clusters share a column
 // (each doubling costs a little for the slowest of more blocks), and with very few the segments
 // run side by side in two passes (twice the rounds, three launches).
-bool make_plan(Plan &pl, Residency &r, const void *kernel, int threads, size_t smem, int64_t columns, int64_t tiles, int most_segs) {
+bool make_plan(Plan &pl, Residency &r, const void *kernel, int threads, size_t smem, int most_blocks, int64_t columns, int64_t tiles,
+               int most_segs) {
     double best = 1e300;
     pl.columns = columns;
-    for (int k = 0; (1 << k) <= kMaxCluster; ++k) {
+    for (int k = 0; (1 << k) <= most_blocks; ++k) {
         const int c = 1 << k;
         if (c > 1 && c / 2 >= tiles) break;
         const int n = clusters_resident(r, kernel, threads, smem, k);
@@ -924,6 +1144,7 @@ bool make_plan(Plan &pl, Residency &r, const void *kernel, int threads, size_t s
         const double per = 1.0 + 0.03 * k;
         consider(rounds, false, double(ceil_div(columns, n)) * double(rounds) * per);
         for (int64_t segs = 2; segs <= std::min<int64_t>(most_segs, rounds); ++segs) {
+            if (segs * c > most_parts(columns)) break;
             const int64_t iters = ceil_div(rounds, segs), items = columns * ceil_div(rounds, iters);
             if (columns >= n) consider(iters, false, double(ceil_div(items, n)) * double(iters) * per + 1.0);
             if (c == 1) consider(iters, true, 2.0 * double(ceil_div(items, n)) * double(iters) + 6.0);
@@ -940,9 +1161,9 @@ ssm_status launch_fwd(FwdArgs<T> p, const Maps3 &tm, bool pairs, cudaStream_t st
     const auto kernel = gated_fwd_kernel<T, K, LOAD>;
     const int64_t columns = p.s.B * p.s.groups, n = p.s.B * p.s.D;
     const int segs = max_segs(columns, ceil_div(p.s.L, kChunk));
-    if (!make_plan(p.pl, resident, reinterpret_cast<const void *>(kernel), threads, smem, columns, ceil_div(p.s.L, kW * K), segs))
+    if (!make_plan(p.pl, resident, reinterpret_cast<const void *>(kernel), threads, smem, FwdShared<T, K>::kMaxCluster, columns,
+                   ceil_div(p.s.L, kW * K), segs))
         return SSM_ERR_CUDA;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess) return SSM_ERR_CUDA;
     unsigned char *ws = reinterpret_cast<unsigned char *>(p.counter);
     p.status = p.counter + 1;
     p.starts = reinterpret_cast<unsigned long long *>(ws + kWsHeader);
@@ -1009,40 +1230,83 @@ ssm_status run_fwd(const ssm_gated_args *a, cudaStream_t st) {
     p.y = static_cast<T *>(a->y), p.h_last = a->h_last, p.states = a->states;
     const bool pairs = a->dim % 2 == 0 && even(a->x_stride) && even(a->r_stride) && even(a->i_stride) && aligned(a->x, 2 * es) &&
                        aligned(a->r, 2 * es) && aligned(a->i, 2 * es) && aligned(a->y, 2 * es);
-    constexpr int KT = es == 2 ? 16 : 8;
+    const auto maps_of = [&](Maps3 &tm, int rows) {
+        return pairs && token_map(&tm.x, a->x, a->dtype, a->batch, a->seqlen, a->dim, a->x_stride, rows) &&
+               token_map(&tm.r, a->r, a->dtype, a->batch, a->seqlen, a->dim, a->r_stride, rows) &&
+               token_map(&tm.i, a->i, a->dtype, a->batch, a->seqlen, a->dim, a->i_stride, rows);
+    };
+    constexpr int K = es == 2 ? 16 : 8;  // stages of 48 KB; half of it where the loading warps are what counts
     Maps3 tm = {};
-    if (pairs && token_map(&tm.x, a->x, a->dtype, a->batch, a->seqlen, a->dim, a->x_stride, kW * KT) &&
-        token_map(&tm.r, a->r, a->dtype, a->batch, a->seqlen, a->dim, a->r_stride, kW * KT) &&
-        token_map(&tm.i, a->i, a->dtype, a->batch, a->seqlen, a->dim, a->i_stride, kW * KT))
-        return launch_fwd<T, KT, kTma>(p, tm, pairs, st);
-    if (pairs || es == 4) return launch_fwd<T, 8, kAsync>(p, tm, pairs, st);
-    if constexpr (es == 2) return launch_fwd<T, 8, kPlain>(p, tm, pairs, st);
+    if (maps_of(tm, kW * K)) return launch_fwd<T, K, kTma>(p, tm, pairs, st);
+    if (pairs || es == 4) return launch_fwd<T, K / 2, kAsync>(p, tm, pairs, st);
+    if constexpr (es == 2) return launch_fwd<T, K / 2, kPlain>(p, tm, pairs, st);
     return SSM_ERR_UNSUPPORTED;
 }
 
-template <typename T, int V>
+template <typename T, int K, Load LOAD>
+ssm_status launch_bwd(BwdArgs<T> p, const Maps7 &tm, bool pairs, float *dlam, cudaStream_t st) {
+    static Residency resident;
+    constexpr size_t smem = sizeof(BwdShared<T, K>);
+    constexpr int threads = (kW + 1 + kLoaders<LOAD>) * 32;
+    const auto kernel = gated_bwd_kernel<T, K, LOAD>;
+    const int64_t columns = p.s.B * p.s.groups, n = p.s.B * p.s.D;
+    const int segs = max_segs(columns, ceil_div(p.s.L, kChunk));
+    if (!make_plan(p.pl, resident, reinterpret_cast<const void *>(kernel), threads, smem, BwdShared<T, K>::kMaxCluster, columns,
+                   ceil_div(p.s.L, kW * K), segs))
+        return SSM_ERR_CUDA;
+    unsigned char *ws = reinterpret_cast<unsigned char *>(p.counter);
+    p.status = p.counter + 1;
+    p.starts = reinterpret_cast<unsigned long long *>(ws + kWsHeader);
+    Map *maps = reinterpret_cast<Map *>(ws + kWsHeader + up256(size_t(n) * size_t(segs) * 8));
+    p.parts = reinterpret_cast<float *>(ws + carry_bytes(p.s.B, p.s.L, p.s.D));
+    if (p.pl.segs > 1 && !p.pl.local && cudaMemsetAsync(ws, 0, kWsHeader + size_t(n) * size_t(p.pl.segs) * 8, st) != cudaSuccess)
+        return SSM_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(p.pl.grid)), cfg.blockDim = dim3(unsigned(threads)), cfg.dynamicSmemBytes = smem, cfg.stream = st;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = unsigned(p.pl.cluster), at.val.clusterDim.y = 1, at.val.clusterDim.z = 1;
+    cfg.attrs = &at, cfg.numAttrs = 1;
+    if (p.pl.local) {
+        p.maps = maps;
+        if (cudaLaunchKernelEx(&cfg, kernel, p, tm, pairs) != cudaSuccess) return SSM_ERR_CUDA;
+        p.maps = nullptr;
+        gated_starts_kernel<<<unsigned(ceil_div(n, 128)), 128, 0, st>>>(n, p.pl.segs, p.dh_last, maps, p.starts);
+    }
+    if (cudaLaunchKernelEx(&cfg, kernel, p, tm, pairs) != cudaSuccess) return SSM_ERR_CUDA;
+    gated_dlam_kernel<<<unsigned(ceil_div(p.s.D, 32)), 1024, 0, st>>>(int64_t(p.pl.segs) * p.pl.cluster * kW * p.s.B, p.s.D, p.s.c, p.parts,
+                                                                      p.lam, dlam);
+    return launched();
+}
+
+template <typename T>
 ssm_status run_bwd(const ssm_gated_bwd_args *a, cudaStream_t st) {
-    BwdArgs<T> p;
-    p.s = {a->batch, a->seqlen, a->dim, ceil_div(a->dim, 32 * V), ceil_div(a->seqlen, kW * kKB), a->c};
+    constexpr size_t es = sizeof(T);
+    BwdArgs<T> p = {};
+    p.s = {a->batch, a->seqlen, a->dim, ceil_div(a->dim, 64), 0, a->c};
+    p.counter = static_cast<unsigned int *>(a->workspace);
     p.x = static_cast<const T *>(a->x), p.r = static_cast<const T *>(a->r), p.i = static_cast<const T *>(a->i);
     p.dy = static_cast<const T *>(a->dy);
     p.xb = a->x_stride[0], p.xt = a->x_stride[1], p.rb = a->r_stride[0], p.rt = a->r_stride[1];
     p.ib = a->i_stride[0], p.it = a->i_stride[1];
-    p.reset = a->reset, p.lam = a->lam, p.states = a->states;
+    p.reset = a->reset, p.lam = a->lam, p.states = a->states, p.dh_last = a->dh_last;
     p.dx = static_cast<T *>(a->dx), p.dr = static_cast<T *>(a->dr), p.di = static_cast<T *>(a->di), p.dh0 = a->dh0;
-    const int64_t n = a->batch * a->dim;
-    unsigned char *ws = static_cast<unsigned char *>(a->workspace);
-    p.maps = reinterpret_cast<Map *>(ws);
-    ws += up256(size_t(n) * size_t(p.s.tiles) * sizeof(Map));
-    p.starts = reinterpret_cast<float *>(ws);
-    ws += up256(size_t(n) * size_t(p.s.tiles + 1) * 4);
-    p.parts = reinterpret_cast<float *>(ws);
-    const unsigned grid = unsigned(a->batch * p.s.groups * p.s.tiles);
-    gated_bwd_kernel<T, V, false><<<grid, kW * 32, 0, st>>>(p);
-    gated_chain_kernel<<<unsigned(ceil_div(n, 128)), 128, 0, st>>>(n, p.s.tiles, true, a->dh_last, p.maps, p.starts);
-    gated_bwd_kernel<T, V, true><<<grid, kW * 32, 0, st>>>(p);
-    gated_dlam_kernel<<<unsigned(ceil_div(a->dim, 32)), 256, 0, st>>>(a->batch * p.s.tiles, a->dim, a->c, p.parts, a->lam, a->dlam);
-    return launched();
+    bool pairs = a->dim % 2 == 0 && even(a->x_stride) && even(a->r_stride) && even(a->i_stride);
+    for (const void *q : {a->x, a->r, a->i, a->dy, static_cast<const void *>(a->dx), static_cast<const void *>(a->dr),
+                          static_cast<const void *>(a->di)})
+        pairs = pairs && aligned(q, 2 * es);
+    constexpr int K = kChunk / kW;
+    const int64_t whole[2] = {a->seqlen * a->dim, a->dim};
+    const auto map = [&](CUtensorMap &m, const void *q, const int64_t *stride, int rows) {
+        return token_map(&m, q, a->dtype, a->batch, a->seqlen, a->dim, stride, rows);
+    };
+    Maps7 tm = {};
+    if (pairs && map(tm.x, a->x, a->x_stride, kChunk) && map(tm.r, a->r, a->r_stride, kChunk) && map(tm.i, a->i, a->i_stride, kChunk) &&
+        map(tm.dy, a->dy, whole, kChunk) && map(tm.dx, a->dx, whole, K) && map(tm.dr, a->dr, whole, K) && map(tm.di, a->di, whole, K))
+        return launch_bwd<T, K, kTma>(p, tm, pairs, a->dlam, st);
+    if (pairs || es == 4) return launch_bwd<T, K, kAsync>(p, tm, pairs, a->dlam, st);
+    if constexpr (es == 2) return launch_bwd<T, K, kPlain>(p, tm, pairs, a->dlam, st);
+    return SSM_ERR_UNSUPPORTED;
 }
 
 __global__ void gated_dlam_zero_kernel(int64_t D, float *dlam) {
@@ -1117,8 +1381,10 @@ ssm_status ssm_gated_scan_fwd(const ssm_gated_args *a, void *stream) {
 
 size_t ssm_gated_scan_bwd_workspace_size(const ssm_gated_bwd_args *a) {
     if (check_common(a) != SSM_OK) return 0;
-    const size_t n = size_t(a->batch) * size_t(a->dim), t = size_t(ceil_div(a->seqlen, kChunk));
-    return up256(n * t * sizeof(Map)) + up256(n * (t + 1) * 4) + up256(n * t * 4);
+    if (a->batch == 0 || a->dim == 0) return 0;
+    const int64_t columns = a->batch * ceil_div(a->dim, 64);
+    return carry_bytes(a->batch, a->seqlen, a->dim) +
+           size_t(a->batch) * size_t(a->dim) * size_t(most_parts(columns)) * kW * 4;
 }
 
 ssm_status ssm_gated_scan_bwd(const ssm_gated_bwd_args *a, void *stream) {
@@ -1151,12 +1417,7 @@ ssm_status ssm_gated_scan_bwd(const ssm_gated_bwd_args *a, void *stream) {
     }
     if (!a->workspace || a->workspace_bytes < ssm_gated_scan_bwd_workspace_size(a)) return SSM_ERR_INVALID;
     if (!aligned(a->workspace, 16)) return SSM_ERR_UNSUPPORTED;
-    bool two = a->dim % 2 == 0 && even(a->x_stride) && even(a->r_stride) && even(a->i_stride);
-    for (const void *q : {a->x, a->r, a->i, a->dy, static_cast<const void *>(a->dx), static_cast<const void *>(a->dr),
-                          static_cast<const void *>(a->di)})
-        two = two && aligned(q, 2 * es);
-    if (a->dtype == SSM_BF16) return two ? run_bwd<__nv_bfloat16, 2>(a, st) : run_bwd<__nv_bfloat16, 1>(a, st);
-    return two ? run_bwd<float, 2>(a, st) : run_bwd<float, 1>(a, st);
+    return a->dtype == SSM_BF16 ? run_bwd<__nv_bfloat16>(a, st) : run_bwd<float>(a, st);
 }
 
 ssm_status ssm_gated_step(int64_t batch, int64_t dim, ssm_dtype dtype, float c, const void *x, int64_t x_stride,

@@ -5,9 +5,12 @@ The bounds follow the arithmetic (u = 2^-24, half a float32 step), to first orde
 a sigmoid from an exponential of 2^-22 and a reciprocal of 2^-23 is off by at most
 (|v| + 7) u, 13 u for |v| <= 6; the rate by 4 u; 1 - exp(-w) by the sum and its own 4 u: 22 u
 relative, so a decay a by 22 u (1 - a) + u; the input's factors by 40 u. They pass through the
-recurrence with the state itself: E_t = a_t E_{t-1} + da_t |h_{t-1}| + 40 u |b_t| + 2 u |h_t|.
-Splitting time into pieces adds roundings of the carried term only, which 2 u |h_t| at each step
-covers. A value stored in the tokens' type adds half a step of that type.
+recurrence with the state itself: E_t = a_t E_{t-1} + da_t |h_{t-1}| + 40 u |b_t| + 2 u M_t, where
+M_t = a_t M_{t-1} + |b_t|. The roundings go by M_t and not by |h_t|: where time is cut into pieces, a
+state is the sum P h + H of what was carried in and what the piece added, each rounded on its own
+(half a step of up to |P h| and of up to the piece's sum of |b| carried on, together at most M_t),
+and the two may cancel. A piece of n steps takes part in fewer than n such sums, so two
+roundings a step cover them. A value stored in the tokens' type adds half a step of that type.
 """
 import torch
 
@@ -32,7 +35,7 @@ def gated_scan(x, r, i, lam, h0=None, reset=None, c=8.0):
     b = beta * si * xd
     B, L, D = x.shape
     h = torch.zeros(B, D, dtype=torch.float64) if h0 is None else h0.double()
-    err = torch.zeros_like(h)
+    err, mag = torch.zeros_like(h), h.abs()
     ys, es = torch.empty_like(b), torch.empty_like(b)
     for t in range(L):
         at = a[:, t]
@@ -41,8 +44,9 @@ def gated_scan(x, r, i, lam, h0=None, reset=None, c=8.0):
         if reset is not None:  # dropped, whatever it was
             fresh = reset[:, t, None]
             hn = torch.where(fresh, b[:, t], hn)
-            h, err = h.masked_fill(fresh, 0.0), err.masked_fill(fresh, 0.0)
-        err = at * err + da * h.abs() + 40 * U * b[:, t].abs() + 2 * U * hn.abs()
+            h, err, mag = h.masked_fill(fresh, 0.0), err.masked_fill(fresh, 0.0), mag.masked_fill(fresh, 0.0)
+        mag = at * mag + b[:, t].abs()
+        err = at * err + da * h.abs() + 40 * U * b[:, t].abs() + 2 * U * mag
         h = hn
         ys[:, t], es[:, t] = h, err
     return ys, 2 * es
@@ -57,13 +61,14 @@ def gated_scan_bwd(x, r, i, lam, dy, h0=None, dh_last=None, reset=None, c=8.0):
     u = si * xd
     start = torch.zeros(B, D, dtype=torch.float64) if h0 is None else h0.double()
     v = torch.zeros_like(start) if dh_last is None else dh_last.double()
-    ev = torch.zeros_like(v)
+    ev, mv = torch.zeros_like(v), v.abs()
     g = {k: torch.empty_like(xd) for k in ("dx", "dr", "di")}
     e = {k: torch.empty_like(xd) for k in ("dx", "dr", "di")}
     dlam, elam, mlam = torch.zeros_like(lam), torch.zeros_like(lam), torch.zeros_like(lam)
     for t in range(L - 1, -1, -1):
         v = v + dy[:, t].double()
-        ev = ev + 2 * U * v.abs()
+        mv = mv + dy[:, t].double().abs()
+        ev = ev + 2 * U * mv
         at, bt, ut = a[:, t], beta[:, t], u[:, t]
         prev = ys[:, t - 1] if t else start
         eprev = es[:, t - 1] if t else torch.zeros_like(start)
@@ -83,13 +88,13 @@ def gated_scan_bwd(x, r, i, lam, dy, h0=None, dh_last=None, reset=None, c=8.0):
         mlam = mlam + (dw * sr[:, t]).abs().sum(0)
         da = torch.where(at == 0, 0.0, 22 * U * (1 - at) + U)
         ev = at * ev + da * v.abs()
-        v = at * v
+        v, mv = at * v, at * mv
         if reset is not None:
-            v, ev = v.masked_fill(fresh, 0.0), ev.masked_fill(fresh, 0.0)
+            v, ev, mv = v.masked_fill(fresh, 0.0), ev.masked_fill(fresh, 0.0), mv.masked_fill(fresh, 0.0)
     k = c * torch.sigmoid(lam)
     # dlam: a tile sums 64 steps one by one and across its warps, then tiles; 200 u covers any order
     g["dlam"], e["dlam"] = dlam * k, k * (elam + 200 * U * mlam)
-    g["dh0"], e["dh0"] = v, ev + 2 * U * v.abs()
+    g["dh0"], e["dh0"] = v, ev + 2 * U * mv
     return g, {n: 2 * t for n, t in e.items()}
 
 
