@@ -14,7 +14,6 @@ device, the calls raise.
     y = gated_step(x_t, r_t, i_t, lam, h)                    # one token of it, h [B, D] updated in place
     y, s = layer_norm(x, weight, bias, residual)             # s = x + residual, y its layer norm
 """
-import contextlib
 import ctypes
 
 import torch
@@ -466,65 +465,112 @@ def selective_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, *, del
     return (y, h_last) if return_last_state else y
 
 
-def _on_stream(stream, s, tensors):
-    """For a caller's stream: the context in which outputs and scratch are allocated (they
-    then belong to that stream), the inputs being held until the stream has read them."""
-    if stream is None or s.cuda_stream == torch.cuda.current_stream(s.device).cuda_stream:
-        return contextlib.nullcontext()
-    for t in tensors:
-        if t is not None:
-            t.record_stream(s)
-    return torch.cuda.stream(s)
+# ----------------------------------------------------- gated recurrence, layer norm
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _need_strided(t, name, shape, dtype, device):
-    """As _need, for tokens [.., D] whose channels are neighbours in memory but whose leading
+class _Launch:
+    """Where a call's work goes: enters with the stream's handle. Outputs and scratch are allocated
+    inside, so that they belong to that stream; on a caller's stream other than the current one the inputs
+    are held until it has read them."""
+    __slots__ = ("handle", "contexts")
+
+    def __init__(self, dev, stream, tensors):
+        self.contexts = ()
+        if stream is None:
+            if torch.cuda.current_device() != dev.index:
+                self.contexts = (torch.cuda.device(dev),)
+            self.handle = _raw_stream(dev.index)
+        else:
+            self.handle = _resolve_stream(stream, dev).cuda_stream
+            if self.handle != _raw_stream(dev.index):
+                for t in tensors:
+                    if t is not None:
+                        t.record_stream(stream)
+            self.contexts = (torch.cuda.device(dev), torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+        return False
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check(t, name, shape, dtype, device):
+    """_need, quick where nothing is wrong."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.is_cuda and t.device == device
+            and t.is_contiguous()):
+        _need(t, name, shape, dtype, device)
+
+
+def _check_strided(t, name, shape, dtype, device):
+    """As _check, for tokens [.., D] whose channels are neighbours in memory but whose leading
     dimensions may have any stride; returns those strides (0 where the size is 1)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device or t.device.type != "cuda":
+    if not t.is_cuda or t.device != device:
         raise ValueError(f"{name}: must be on {device} (a CUDA device)")
-    if shape[-1] > 1 and t.stride(-1) != 1:
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the channels must be contiguous (stride 1 in the last dimension)")
-    return [t.stride(k) if shape[k] > 1 else 0 for k in range(len(shape) - 1)]
+    return tuple(v if n > 1 else 0 for v, n in zip(st[:-1], shape))
 
 
-def _gated_common(a, x, r, i, lam, reset, c, h0):
-    """Check and fill in what the gated scan's forward and backward take alike."""
+def _scratch(nbytes, workspace, dev):
+    """A call's workspace: the caller's, or fresh memory of the current stream."""
+    if workspace is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+    ws = workspace.get(nbytes, dev) if isinstance(workspace, ScanWorkspace) else workspace
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    if ws.numel() * ws.element_size() < nbytes:
+        raise ValueError(f"workspace too small: {ws.numel() * ws.element_size()} < {nbytes} bytes")
+    return ws
+
+
+def _gated_head(x, r, i, lam, reset, c, h0):
+    """Check what the gated scan's forward and backward take alike: the argument structs' first fields."""
     dev, tok = x.device, x.dtype
     if tok not in _TOKEN_DTYPES:
         raise TypeError(f"x: dtype must be float32 or bfloat16, got {tok}")
     if x.dim() != 3:
         raise ValueError("x must be [B, L, D]")
-    Bsz, L, Dm = x.shape
-    for t, name in ((x, "x"), (r, "r"), (i, "i")):
-        getattr(a, name + "_stride")[:] = _need_strided(t, name, (Bsz, L, Dm), tok, dev)
-    _need(lam, "lam", (Dm,), torch.float32, dev)
+    shape = x.shape
+    Bsz, L, Dm = shape
+    sx, sr, si = (_check_strided(t, name, shape, tok, dev) for t, name in ((x, "x"), (r, "r"), (i, "i")))
+    _check(lam, "lam", (Dm,), torch.float32, dev)
     if reset is not None:
-        _need(reset, "reset", (Bsz, L), torch.bool, dev)
+        _check(reset, "reset", (Bsz, L), torch.bool, dev)
     if h0 is not None:
-        _need(h0, "h0", (Bsz, Dm), torch.float32, dev)
-    a.batch, a.seqlen, a.dim, a.dtype, a.flags, a.c = Bsz, L, Dm, _TOKEN_DTYPES[tok], 0, c
-    a.x, a.r, a.i, a.reset, a.lam = (_ptr(t) for t in (x, r, i, reset, lam))
-    return Bsz, L, Dm
+        _check(h0, "h0", (Bsz, Dm), torch.float32, dev)
+    return (Bsz, L, Dm, _TOKEN_DTYPES[tok], 0, c, x.data_ptr(), r.data_ptr(), i.data_ptr(), sx, sr, si, _at(reset),
+            lam.data_ptr())
 
 
-def _scratch(a, nbytes, workspace, dev):
-    """The call's workspace: the caller's, or fresh memory of the current stream."""
-    if workspace is None:
-        ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
-    else:
-        ws = workspace.get(nbytes, dev) if isinstance(workspace, ScanWorkspace) else workspace
-    if ws.device != dev or not ws.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {dev}")
-    a.workspace, a.workspace_bytes = _ptr(ws), ws.numel() * ws.element_size()
-    if a.workspace_bytes < nbytes:
-        raise ValueError(f"workspace too small: {a.workspace_bytes} < {nbytes} bytes")
-    return ws
+def _gated_states(Bsz, L, Dm, dev):
+    return torch.empty((Bsz, -(-L // _native.SSM_GATED_CHUNK), Dm), dtype=torch.float32, device=dev)
+
+
+def _gated_fwd(head, h0, y, h_last, states, workspace, dev, handle):
+    lib = _native.lib()
+    a = _native.GatedArgs(*head, _at(h0), _at(y), _at(h_last), _at(states))
+    ref = ctypes.byref(a)
+    ws = _scratch(lib.ssm_gated_scan_workspace_size(ref), workspace, dev)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    _native.check(lib.ssm_gated_scan_fwd(ref, handle), "ssm_gated_scan_fwd")
 
 
 def gated_scan_fwd(x, r, i, lam, h0=None, *, reset=None, c=8.0, return_last_state=False, return_states=False,
@@ -539,29 +585,22 @@ def gated_scan_fwd(x, r, i, lam, h0=None, *, reset=None, c=8.0, return_last_stat
     [B, D] float32, and with return_states the states that gated_scan_bwd takes
     ([B, ceil(L / 64), D] float32).
     """
-    a = _native.GatedArgs()
-    Bsz, L, Dm = _gated_common(a, x, r, i, lam, reset, c, h0)
+    head = _gated_head(x, r, i, lam, reset, c, h0)
+    Bsz, L, Dm = x.shape
     dev, tok = x.device, x.dtype
-    lib = _native.lib()
-    s = _resolve_stream(stream, dev)
-    with torch.cuda.device(dev), _on_stream(stream, s, (x, r, i, lam, reset, h0, out, h_last)):
+    with _Launch(dev, stream, (x, r, i, lam, reset, h0, out, h_last)) as handle:
         y = torch.empty((Bsz, L, Dm), dtype=tok, device=dev) if out is None else out
-        _need(y, "out", (Bsz, L, Dm), tok, dev)
-        if return_last_state and h_last is None:
-            h_last = torch.empty((Bsz, Dm), dtype=torch.float32, device=dev)
+        if out is not None:
+            _check(y, "out", (Bsz, L, Dm), tok, dev)
         if h_last is not None:
-            _need(h_last, "h_last", (Bsz, Dm), torch.float32, dev)
+            _check(h_last, "h_last", (Bsz, Dm), torch.float32, dev)
+        elif return_last_state:
+            h_last = torch.empty((Bsz, Dm), dtype=torch.float32, device=dev)
         states = _gated_states(Bsz, L, Dm, dev) if return_states else None
-        a.h0, a.y, a.h_last, a.states = (_ptr(t) for t in (h0, y, h_last, states))
-        ws = _scratch(a, int(lib.ssm_gated_scan_workspace_size(ctypes.byref(a))), workspace, dev)
-        _native.check(lib.ssm_gated_scan_fwd(ctypes.byref(a), _handle(s)), "ssm_gated_scan_fwd")
-        del ws
-    res = (y,) + ((h_last,) if return_last_state else ()) + ((states,) if return_states else ())
-    return res if len(res) > 1 else y
-
-
-def _gated_states(Bsz, L, Dm, dev):
-    return torch.empty((Bsz, -(-L // _native.SSM_GATED_CHUNK), Dm), dtype=torch.float32, device=dev)
+        _gated_fwd(head, h0, y, h_last, states, workspace, dev, handle)
+    if not return_last_state and not return_states:
+        return y
+    return (y,) + ((h_last,) if return_last_state else ()) + ((states,) if return_states else ())
 
 
 def gated_scan_bwd(x, r, i, lam, dy, h0=None, dh_last=None, *, states=None, reset=None, c=8.0, workspace=None,
@@ -573,34 +612,28 @@ def gated_scan_bwd(x, r, i, lam, dy, h0=None, dh_last=None, *, states=None, rese
 
     Returns a dict: dx, dr, di [B, L, D] in x's dtype, dlam [D] and dh0 [B, D] float32.
     """
-    a = _native.GatedBwdArgs()
-    Bsz, L, Dm = _gated_common(a, x, r, i, lam, reset, c, h0)
+    head = _gated_head(x, r, i, lam, reset, c, h0)
+    shape = Bsz, L, Dm = x.shape
     dev, tok = x.device, x.dtype
-    _need(dy, "dy", (Bsz, L, Dm), tok, dev)
+    _check(dy, "dy", shape, tok, dev)
     if dh_last is not None:
-        _need(dh_last, "dh_last", (Bsz, Dm), torch.float32, dev)
+        _check(dh_last, "dh_last", (Bsz, Dm), torch.float32, dev)
     lib = _native.lib()
-    s = _resolve_stream(stream, dev)
-    with torch.cuda.device(dev), _on_stream(stream, s, (x, r, i, lam, reset, h0, dy, dh_last, states)):
+    with _Launch(dev, stream, (x, r, i, lam, reset, h0, dy, dh_last, states)) as handle:
         if states is None:
             states = _gated_states(Bsz, L, Dm, dev)
-            f = _native.GatedArgs()
-            _gated_common(f, x, r, i, lam, reset, c, h0)
-            f.h0, f.states = _ptr(h0), _ptr(states)
-            ws = _scratch(f, int(lib.ssm_gated_scan_workspace_size(ctypes.byref(f))), None, dev)
-            _native.check(lib.ssm_gated_scan_fwd(ctypes.byref(f), _handle(s)), "ssm_gated_scan_fwd")
-            del ws
-        _need(states, "states", (Bsz, -(-L // _native.SSM_GATED_CHUNK), Dm), torch.float32, dev)
-        tokens = dict(dtype=tok, device=dev)
-        g = dict(dx=torch.empty((Bsz, L, Dm), **tokens), dr=torch.empty((Bsz, L, Dm), **tokens),
-                 di=torch.empty((Bsz, L, Dm), **tokens), dlam=torch.empty((Dm,), dtype=torch.float32, device=dev),
-                 dh0=torch.empty((Bsz, Dm), dtype=torch.float32, device=dev))
-        a.states, a.dy, a.dh_last = _ptr(states), _ptr(dy), _ptr(dh_last)
-        a.dx, a.dr, a.di, a.dlam, a.dh0 = (_ptr(t) for t in g.values())
-        ws = _scratch(a, int(lib.ssm_gated_scan_bwd_workspace_size(ctypes.byref(a))), workspace, dev)
-        _native.check(lib.ssm_gated_scan_bwd(ctypes.byref(a), _handle(s)), "ssm_gated_scan_bwd")
-        del ws
-    return g
+            _gated_fwd(head, h0, None, None, states, None, dev, handle)
+        _check(states, "states", (Bsz, -(-L // _native.SSM_GATED_CHUNK), Dm), torch.float32, dev)
+        dx, dr, di = (torch.empty(shape, dtype=tok, device=dev) for _ in range(3))
+        dlam = torch.empty((Dm,), dtype=torch.float32, device=dev)
+        dh0 = torch.empty((Bsz, Dm), dtype=torch.float32, device=dev)
+        a = _native.GatedBwdArgs(*head, states.data_ptr(), dy.data_ptr(), _at(dh_last), dx.data_ptr(), dr.data_ptr(),
+                                 di.data_ptr(), dlam.data_ptr(), dh0.data_ptr())
+        ref = ctypes.byref(a)
+        ws = _scratch(lib.ssm_gated_scan_bwd_workspace_size(ref), workspace, dev)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+        _native.check(lib.ssm_gated_scan_bwd(ref, handle), "ssm_gated_scan_bwd")
+    return dict(dx=dx, dr=dr, di=di, dlam=dlam, dh0=dh0)
 
 
 def gated_step(x, r, i, lam, h, *, c=8.0, h_out=None, out=None, stream=None):
@@ -609,23 +642,25 @@ def gated_step(x, r, i, lam, h, *, c=8.0, h_out=None, out=None, stream=None):
     x, r, i: [B, D], the channels contiguous; lam: [D]; h: [B, D] float32, updated in place,
     or read only when h_out [B, D] is given to take the new state. Returns y [B, D].
     """
-    dev, tok = x.device, x.dtype
+    dev, tok, shape = x.device, x.dtype, x.shape
     if tok not in _TOKEN_DTYPES:
         raise TypeError(f"x: dtype must be float32 or bfloat16, got {tok}")
-    if x.dim() != 2:
+    if len(shape) != 2:
         raise ValueError("x must be [B, D]")
-    Bsz, Dm = x.shape
-    strides = [_need_strided(t, name, (Bsz, Dm), tok, dev)[0] for t, name in ((x, "x"), (r, "r"), (i, "i"))]
-    _need(lam, "lam", (Dm,), torch.float32, dev)
-    _need(h, "h", (Bsz, Dm), torch.float32, dev)
-    h_out = h if h_out is None else h_out
-    _need(h_out, "h_out", (Bsz, Dm), torch.float32, dev)
-    s = _resolve_stream(stream, dev)
-    with torch.cuda.device(dev), _on_stream(stream, s, (x, r, i, lam, h, h_out, out)):
+    Bsz, Dm = shape
+    sx, sr, si = (_check_strided(t, name, shape, tok, dev)[0] for t, name in ((x, "x"), (r, "r"), (i, "i")))
+    _check(lam, "lam", (Dm,), torch.float32, dev)
+    _check(h, "h", shape, torch.float32, dev)
+    if h_out is None:
+        h_out = h
+    else:
+        _check(h_out, "h_out", shape, torch.float32, dev)
+    with _Launch(dev, stream, (x, r, i, lam, h, h_out, out)) as handle:
         y = torch.empty((Bsz, Dm), dtype=tok, device=dev) if out is None else out
-        _need(y, "out", (Bsz, Dm), tok, dev)
-        rc = _native.lib().ssm_gated_step(Bsz, Dm, _TOKEN_DTYPES[tok], c, _ptr(x), strides[0], _ptr(r), strides[1],
-                                          _ptr(i), strides[2], _ptr(lam), _ptr(h), _ptr(h_out), _ptr(y), _handle(s))
+        if out is not None:
+            _check(y, "out", shape, tok, dev)
+        rc = _native.lib().ssm_gated_step(Bsz, Dm, _TOKEN_DTYPES[tok], c, x.data_ptr(), sx, r.data_ptr(), sr, i.data_ptr(),
+                                          si, lam.data_ptr(), h.data_ptr(), h_out.data_ptr(), y.data_ptr(), handle)
     _native.check(rc, "ssm_gated_step")
     return y
 
@@ -678,31 +713,34 @@ def layer_norm_fwd(x, weight, bias=None, residual=None, *, eps=1e-5, out=None, r
     residual in float32 (residual_out, which may be residual itself); with return_stats also the
     rows' mean and 1 / sqrt(var + eps), float32.
     """
-    dev, tok = x.device, x.dtype
+    dev, tok, shape = x.device, x.dtype, x.shape
     rows, Dm = _norm_shape(x, "x")
-    _need(x, "x", x.shape, tok, dev)
-    _need(weight, "weight", (Dm,), torch.float32, dev)
+    f32 = torch.float32
+    _check(x, "x", shape, tok, dev)
+    _check(weight, "weight", (Dm,), f32, dev)
     if bias is not None:
-        _need(bias, "bias", (Dm,), torch.float32, dev)
+        _check(bias, "bias", (Dm,), f32, dev)
     if residual is not None:
-        _need(residual, "residual", x.shape, torch.float32, dev)
+        _check(residual, "residual", shape, f32, dev)
     elif residual_out is not None:
         raise ValueError("residual_out needs residual")
-    s = _resolve_stream(stream, dev)
-    with torch.cuda.device(dev), _on_stream(stream, s, (x, weight, bias, residual, out, residual_out)):
-        y = torch.empty_like(x) if out is None else out
-        _need(y, "out", x.shape, tok, dev)
-        if residual is not None:
-            residual_out = torch.empty_like(residual) if residual_out is None else residual_out
-            _need(residual_out, "residual_out", x.shape, torch.float32, dev)
-        stats = torch.empty((2,) + x.shape[:-1], dtype=torch.float32, device=dev) if return_stats else (None, None)
-        a = _native.NormArgs()
-        a.rows, a.dim, a.dtype, a.eps = rows, Dm, _TOKEN_DTYPES[tok], eps
-        a.x, a.weight, a.bias, a.residual, a.y, a.residual_out, a.mean, a.rstd = (
-            _ptr(t) for t in (x, weight, bias, residual, y, residual_out, stats[0], stats[1]))
-        _native.check(_native.lib().ssm_layer_norm_fwd(ctypes.byref(a), _handle(s)), "ssm_layer_norm_fwd")
-    res = (y,) + ((residual_out,) if residual is not None else ()) + ((stats[0], stats[1]) if return_stats else ())
-    return res if len(res) > 1 else y
+    with _Launch(dev, stream, (x, weight, bias, residual, out, residual_out)) as handle:
+        y = torch.empty(shape, dtype=tok, device=dev) if out is None else out
+        if out is not None:
+            _check(y, "out", shape, tok, dev)
+        if residual_out is not None:
+            _check(residual_out, "residual_out", shape, f32, dev)
+        elif residual is not None:
+            residual_out = torch.empty(shape, dtype=f32, device=dev)
+        mean = rstd = None
+        if return_stats:
+            mean, rstd = torch.empty((2,) + shape[:-1], dtype=f32, device=dev).unbind(0)
+        a = _native.NormArgs(rows, Dm, _TOKEN_DTYPES[tok], eps, x.data_ptr(), weight.data_ptr(), _at(bias), _at(residual),
+                             y.data_ptr(), _at(residual_out), _at(mean), _at(rstd))
+        _native.check(_native.lib().ssm_layer_norm_fwd(ctypes.byref(a), handle), "ssm_layer_norm_fwd")
+    if residual is None and not return_stats:
+        return y
+    return (y,) + ((residual_out,) if residual is not None else ()) + ((mean, rstd) if return_stats else ())
 
 
 def layer_norm_bwd(dy, s, weight, mean, rstd, dresidual_out=None, *, residual=False, bias=True, workspace=None,
@@ -714,33 +752,32 @@ def layer_norm_bwd(dy, s, weight, mean, rstd, dresidual_out=None, *, residual=Fa
     Returns a dict: dx in dy's dtype; dweight and (None without bias) dbias [D] float32;
     with residual dresidual in float32 (dx itself for float32 tokens), else None.
     """
-    dev, tok = dy.device, dy.dtype
+    dev, tok, shape = dy.device, dy.dtype, dy.shape
     rows, Dm = _norm_shape(dy, "dy")
     f32 = torch.float32
-    _need(dy, "dy", dy.shape, tok, dev)
-    _need(s, "s", dy.shape, f32 if residual else tok, dev)
-    _need(weight, "weight", (Dm,), f32, dev)
-    _need(mean, "mean", dy.shape[:-1], f32, dev)
-    _need(rstd, "rstd", dy.shape[:-1], f32, dev)
+    _check(dy, "dy", shape, tok, dev)
+    _check(s, "s", shape, f32 if residual else tok, dev)
+    _check(weight, "weight", (Dm,), f32, dev)
+    _check(mean, "mean", shape[:-1], f32, dev)
+    _check(rstd, "rstd", shape[:-1], f32, dev)
     if dresidual_out is not None:
         if not residual:
             raise ValueError("dresidual_out needs residual")
-        _need(dresidual_out, "dresidual_out", dy.shape, f32, dev)
+        _check(dresidual_out, "dresidual_out", shape, f32, dev)
     lib = _native.lib()
-    st = _resolve_stream(stream, dev)
-    with torch.cuda.device(dev), _on_stream(stream, st, (dy, s, weight, mean, rstd, dresidual_out)):
-        dx = torch.empty_like(dy)
-        two = residual and tok != f32
-        dres = torch.empty(dy.shape, dtype=f32, device=dev) if two else None
+    with _Launch(dev, stream, (dy, s, weight, mean, rstd, dresidual_out)) as handle:
+        dx = torch.empty(shape, dtype=tok, device=dev)
+        two = residual and tok is not f32
+        dres = torch.empty(shape, dtype=f32, device=dev) if two else None
         dweight = torch.empty((Dm,), dtype=f32, device=dev)
         dbias = torch.empty((Dm,), dtype=f32, device=dev) if bias else None
-        a = _native.NormBwdArgs()
-        a.rows, a.dim, a.dtype, a.has_residual = rows, Dm, _TOKEN_DTYPES[tok], int(residual)
-        a.s, a.dy, a.weight, a.mean, a.rstd, a.dresidual_out, a.dx, a.dresidual, a.dweight, a.dbias = (
-            _ptr(t) for t in (s, dy, weight, mean, rstd, dresidual_out, dx, dres, dweight, dbias))
-        ws = _scratch(a, int(lib.ssm_layer_norm_bwd_workspace_size(ctypes.byref(a))), workspace, dev)
-        _native.check(lib.ssm_layer_norm_bwd(ctypes.byref(a), _handle(st)), "ssm_layer_norm_bwd")
-        del ws
+        a = _native.NormBwdArgs(rows, Dm, _TOKEN_DTYPES[tok], int(residual), s.data_ptr(), dy.data_ptr(), weight.data_ptr(),
+                                mean.data_ptr(), rstd.data_ptr(), _at(dresidual_out), dx.data_ptr(), _at(dres),
+                                dweight.data_ptr(), _at(dbias))
+        ref = ctypes.byref(a)
+        ws = _scratch(lib.ssm_layer_norm_bwd_workspace_size(ref), workspace, dev)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+        _native.check(lib.ssm_layer_norm_bwd(ref, handle), "ssm_layer_norm_bwd")
     return dict(dx=dx, dweight=dweight, dbias=dbias, dresidual=(dres if two else dx) if residual else None)
 
 

@@ -1143,7 +1143,7 @@ bool make_plan(Plan &pl, Residency &r, const void *kernel, int threads, size_t s
         };
         const double per = 1.0 + 0.03 * k;
         consider(rounds, false, double(ceil_div(columns, n)) * double(rounds) * per);
-        for (int64_t segs = 2; segs <= std::min<int64_t>(most_segs, rounds); ++segs) {
+        for (int64_t segs = 2; segs <= std::min<int64_t>(most_segs, rounds); segs += std::max<int64_t>(1, segs / 4)) {
             if (segs * c > most_parts(columns)) break;
             const int64_t iters = ceil_div(rounds, segs), items = columns * ceil_div(rounds, iters);
             if (columns >= n) consider(iters, false, double(ceil_div(items, n)) * double(iters) * per + 1.0);
