@@ -618,22 +618,28 @@ def gated_scan_bwd(x, r, i, lam, dy, h0=None, dh_last=None, *, states=None, rese
     _check(dy, "dy", shape, tok, dev)
     if dh_last is not None:
         _check(dh_last, "dh_last", (Bsz, Dm), torch.float32, dev)
-    lib = _native.lib()
     with _Launch(dev, stream, (x, r, i, lam, reset, h0, dy, dh_last, states)) as handle:
         if states is None:
             states = _gated_states(Bsz, L, Dm, dev)
             _gated_fwd(head, h0, None, None, states, None, dev, handle)
         _check(states, "states", (Bsz, -(-L // _native.SSM_GATED_CHUNK), Dm), torch.float32, dev)
-        dx, dr, di = (torch.empty(shape, dtype=tok, device=dev) for _ in range(3))
-        dlam = torch.empty((Dm,), dtype=torch.float32, device=dev)
-        dh0 = torch.empty((Bsz, Dm), dtype=torch.float32, device=dev)
-        a = _native.GatedBwdArgs(*head, states.data_ptr(), dy.data_ptr(), _at(dh_last), dx.data_ptr(), dr.data_ptr(),
-                                 di.data_ptr(), dlam.data_ptr(), dh0.data_ptr())
-        ref = ctypes.byref(a)
-        ws = _scratch(lib.ssm_gated_scan_bwd_workspace_size(ref), workspace, dev)
-        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-        _native.check(lib.ssm_gated_scan_bwd(ref, handle), "ssm_gated_scan_bwd")
+        dx, dr, di, dlam, dh0 = _gated_bwd(head, x, states, dy, dh_last, workspace, handle)
     return dict(dx=dx, dr=dr, di=di, dlam=dlam, dh0=dh0)
+
+
+def _gated_bwd(head, x, states, dy, dh_last, workspace, handle):
+    lib, dev = _native.lib(), x.device
+    Bsz, _, Dm = x.shape
+    dx, dr, di = (torch.empty(x.shape, dtype=x.dtype, device=dev) for _ in range(3))
+    dlam = torch.empty((Dm,), dtype=torch.float32, device=dev)
+    dh0 = torch.empty((Bsz, Dm), dtype=torch.float32, device=dev)
+    a = _native.GatedBwdArgs(*head, states.data_ptr(), dy.data_ptr(), _at(dh_last), dx.data_ptr(), dr.data_ptr(),
+                             di.data_ptr(), dlam.data_ptr(), dh0.data_ptr())
+    ref = ctypes.byref(a)
+    ws = _scratch(lib.ssm_gated_scan_bwd_workspace_size(ref), workspace, dev)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    _native.check(lib.ssm_gated_scan_bwd(ref, handle), "ssm_gated_scan_bwd")
+    return dx, dr, di, dlam, dh0
 
 
 def gated_step(x, r, i, lam, h, *, c=8.0, h_out=None, out=None, stream=None):
@@ -665,6 +671,13 @@ def gated_step(x, r, i, lam, h, *, c=8.0, h_out=None, out=None, stream=None):
     return y
 
 
+def _as_grad(g, like, dtype):
+    """An incoming gradient as the kernels take it (zeros where none came)."""
+    if g is None:
+        return torch.zeros(like.shape, dtype=dtype, device=like.device)
+    return g if g.dtype is dtype and g.is_contiguous() else g.to(dtype).contiguous()
+
+
 class _GatedScan(torch.autograd.Function):
     """gated_scan_fwd as an autograd function; of the forward it keeps the inputs and the
     states before every chunk."""
@@ -683,10 +696,12 @@ class _GatedScan(torch.autograd.Function):
         x, r, i, lam, reset, states = ctx.saved_tensors
         if dy is None and dh_last is None:
             return (None,) * 8
-        dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.to(x.dtype).contiguous()
-        dh_last = None if dh_last is None else dh_last.float().contiguous()
-        g = gated_scan_bwd(x, r, i, lam, dy, None, dh_last, states=states, reset=reset, c=ctx.c)
-        return g["dx"], g["dr"], g["di"], g["dlam"], g["dh0"] if ctx.has_h0 else None, None, None, None
+        head = _gated_head(x, r, i, lam, reset, ctx.c, None)
+        dy = _as_grad(dy, x, x.dtype)
+        dh_last = None if dh_last is None else _as_grad(dh_last, lam, torch.float32)
+        with _Launch(x.device, None, ()) as handle:
+            dx, dr, di, dlam, dh0 = _gated_bwd(head, x, states, dy, dh_last, None, handle)
+        return dx, dr, di, dlam, dh0 if ctx.has_h0 else None, None, None, None
 
 
 def gated_scan(x, r, i, lam, h0=None, *, reset=None, c=8.0, return_last_state=False):
@@ -732,9 +747,7 @@ def layer_norm_fwd(x, weight, bias=None, residual=None, *, eps=1e-5, out=None, r
             _check(residual_out, "residual_out", shape, f32, dev)
         elif residual is not None:
             residual_out = torch.empty(shape, dtype=f32, device=dev)
-        mean = rstd = None
-        if return_stats:
-            mean, rstd = torch.empty((2,) + shape[:-1], dtype=f32, device=dev).unbind(0)
+        mean, rstd = (torch.empty(shape[:-1], dtype=f32, device=dev) for _ in range(2)) if return_stats else (None, None)
         a = _native.NormArgs(rows, Dm, _TOKEN_DTYPES[tok], eps, x.data_ptr(), weight.data_ptr(), _at(bias), _at(residual),
                              y.data_ptr(), _at(residual_out), _at(mean), _at(rstd))
         _native.check(_native.lib().ssm_layer_norm_fwd(ctypes.byref(a), handle), "ssm_layer_norm_fwd")
@@ -764,21 +777,26 @@ def layer_norm_bwd(dy, s, weight, mean, rstd, dresidual_out=None, *, residual=Fa
         if not residual:
             raise ValueError("dresidual_out needs residual")
         _check(dresidual_out, "dresidual_out", shape, f32, dev)
-    lib = _native.lib()
     with _Launch(dev, stream, (dy, s, weight, mean, rstd, dresidual_out)) as handle:
-        dx = torch.empty(shape, dtype=tok, device=dev)
-        two = residual and tok is not f32
-        dres = torch.empty(shape, dtype=f32, device=dev) if two else None
-        dweight = torch.empty((Dm,), dtype=f32, device=dev)
-        dbias = torch.empty((Dm,), dtype=f32, device=dev) if bias else None
-        a = _native.NormBwdArgs(rows, Dm, _TOKEN_DTYPES[tok], int(residual), s.data_ptr(), dy.data_ptr(), weight.data_ptr(),
-                                mean.data_ptr(), rstd.data_ptr(), _at(dresidual_out), dx.data_ptr(), _at(dres),
-                                dweight.data_ptr(), _at(dbias))
-        ref = ctypes.byref(a)
-        ws = _scratch(lib.ssm_layer_norm_bwd_workspace_size(ref), workspace, dev)
-        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-        _native.check(lib.ssm_layer_norm_bwd(ref, handle), "ssm_layer_norm_bwd")
-    return dict(dx=dx, dweight=dweight, dbias=dbias, dresidual=(dres if two else dx) if residual else None)
+        dx, dweight, dbias, dres = _norm_bwd(rows, Dm, dy, s, weight, mean, rstd, dresidual_out, residual, bias, workspace, handle)
+    return dict(dx=dx, dweight=dweight, dbias=dbias, dresidual=dres)
+
+
+def _norm_bwd(rows, Dm, dy, s, weight, mean, rstd, dresidual_out, residual, bias, workspace, handle):
+    lib, dev, tok, f32 = _native.lib(), dy.device, dy.dtype, torch.float32
+    dx = torch.empty(dy.shape, dtype=tok, device=dev)
+    two = residual and tok is not f32
+    dres = torch.empty(dy.shape, dtype=f32, device=dev) if two else None
+    dweight = torch.empty((Dm,), dtype=f32, device=dev)
+    dbias = torch.empty((Dm,), dtype=f32, device=dev) if bias else None
+    a = _native.NormBwdArgs(rows, Dm, _TOKEN_DTYPES[tok], int(residual), s.data_ptr(), dy.data_ptr(), weight.data_ptr(),
+                            mean.data_ptr(), rstd.data_ptr(), _at(dresidual_out), dx.data_ptr(), _at(dres),
+                            dweight.data_ptr(), _at(dbias))
+    ref = ctypes.byref(a)
+    ws = _scratch(lib.ssm_layer_norm_bwd_workspace_size(ref), workspace, dev)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    _native.check(lib.ssm_layer_norm_bwd(ref, handle), "ssm_layer_norm_bwd")
+    return dx, dweight, dbias, (dres if two else dx) if residual else None
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -796,10 +814,12 @@ class _LayerNorm(torch.autograd.Function):
         s, weight, mean, rstd = ctx.saved_tensors
         if dy is None and ds is None:
             return (None,) * 5
-        dy = torch.zeros(s.shape, dtype=ctx.tok, device=s.device) if dy is None else dy.to(ctx.tok).contiguous()
-        ds = None if ds is None else ds.float().contiguous()
-        g = layer_norm_bwd(dy, s, weight, mean, rstd, ds, residual=ctx.residual, bias=ctx.has_bias)
-        return g["dx"], g["dweight"], g["dbias"], g["dresidual"], None
+        rows, Dm = _norm_shape(s, "s")
+        dy = _as_grad(dy, s, ctx.tok)
+        ds = None if ds is None else _as_grad(ds, s, torch.float32)
+        with _Launch(s.device, None, ()) as handle:
+            dx, dweight, dbias, dres = _norm_bwd(rows, Dm, dy, s, weight, mean, rstd, ds, ctx.residual, ctx.has_bias, None, handle)
+        return dx, dweight, dbias, dres, None
 
 
 def layer_norm(x, weight, bias=None, residual=None, *, eps=1e-5):
