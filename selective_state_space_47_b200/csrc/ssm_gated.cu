@@ -335,6 +335,25 @@ __device__ __forceinline__ float4 then2(const float4 f, const float4 g) {
     return make_float4(a.P, a.H, b.P, b.H);
 }
 
+// Eight maps in a row, joined two by two: three maps deep instead of seven. The same joints
+// give what enters each of them.
+struct Eight {
+    float4 m[8], two[4], four[2];
+    __device__ __forceinline__ void join() {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) two[k] = then2(m[2 * k], m[2 * k + 1]);
+        four[0] = then2(two[0], two[1]), four[1] = then2(two[2], two[3]);
+    }
+    __device__ __forceinline__ float4 all() const { return then2(four[0], four[1]); }
+    __device__ __forceinline__ void enter(const float2 h, float2 (&e)[8]) const {
+        e[0] = h, e[4] = apply2(four[0], h);
+        e[2] = apply2(two[0], h), e[6] = apply2(two[2], e[4]);
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) e[k + 1] = apply2(m[k], e[k]);
+    }
+};
+static_assert(kW == 8, "");
+
 // ---------------------------------------------------------- cluster plumbing
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -544,13 +563,11 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, 2)
             const uint32_t phase = (it >> 1) & 1;
             if (lane == 0 && C > 1) mbar_arrive_expect_tx(&s.mail[buf], C * sizeof(s.inbox[0][0]));
             wait_phase(&s.posted[buf], phase, &s.abort, p.status);
-            float4 m[kW];
+            Eight f;
 #pragma unroll
-            for (int w = 0; w < kW; ++w) m[w] = s.maps[buf][w][lane];
-            float4 f[kW / 2];
-#pragma unroll
-            for (int w = 0; w < kW / 2; ++w) f[w] = then2(m[2 * w], m[2 * w + 1]);
-            const float4 own = then2(then2(f[0], f[1]), then2(f[2], f[3]));
+            for (int w = 0; w < kW; ++w) f.m[w] = s.maps[buf][w][lane];
+            f.join();
+            const float4 own = f.all();
             if (C > 1)
                 for (unsigned int k = 0; k < C; ++k)
                     send16(peer_addr(&s.inbox[buf][rank][lane], k), own, peer_addr(&s.mail[buf], k));
@@ -581,11 +598,10 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, 2)
                 S = apply2(own, S);
                 if (p.maps) M = then2(M, own);
             }
+            float2 e[kW];
+            f.enter(mine, e);
 #pragma unroll
-            for (int w = 0; w < kW; ++w) {
-                *reinterpret_cast<float2 *>(&s.maps[buf][w][lane]) = mine;
-                mine = apply2(m[w], mine);
-            }
+            for (int w = 0; w < kW; ++w) *reinterpret_cast<float2 *>(&s.maps[buf][w][lane]) = e[w];
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.ready[buf]);
             if ((t.flags & 2) && rank == 0) {
@@ -870,14 +886,15 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, sizeof(T) == 2
                 if (have > 1) hs.y = q[1];
             }
             wait_phase(&s.posted[buf], phase, &s.abort, p.status);
-            float4 m[kW], r[kW];  // the state's maps, and the adjoint's from the last warp to the first
+            Eight r;  // the adjoint's maps, from the last warp to the first
 #pragma unroll
             for (int w = 0; w < kW; ++w) {
-                m[w] = s.maps[buf][w][lane];
+                const float4 m = s.maps[buf][w][lane];
                 const float2 g = s.adj[buf][w][lane];
-                r[kW - 1 - w] = make_float4(m[w].x, g.x, m[w].z, g.y);
+                r.m[kW - 1 - w] = make_float4(m.x, g.x, m.z, g.y);
             }
-            const float4 own = then2(then2(then2(r[0], r[1]), then2(r[2], r[3])), then2(then2(r[4], r[5]), then2(r[6], r[7])));
+            r.join();
+            const float4 own = r.all();
             if (C > 1)
                 for (unsigned int k = 0; k < C; ++k)
                     send16(peer_addr(&s.inbox[buf][rank][lane], k), own, peer_addr(&s.mail[buf], k));
@@ -895,6 +912,13 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, sizeof(T) == 2
                     }
                 }
             }
+            // the states entering the warps' steps, while the mail is under way
+#pragma unroll
+            for (int w = 0; w < kW; ++w) {
+                const float4 m = s.maps[buf][w][lane];
+                *reinterpret_cast<float2 *>(&s.maps[buf][w][lane]) = hs;
+                hs = apply2(m, hs);
+            }
             float2 mine = S;
             if (C > 1) {
                 wait_phase(&s.mail[buf], phase, &s.abort, p.status);
@@ -908,17 +932,10 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, sizeof(T) == 2
                 S = apply2(own, S);
                 if (p.maps) M = then2(M, own);
             }
-            float2 gs[kW];
+            float2 e[kW];
+            r.enter(mine, e);
 #pragma unroll
-            for (int w = 0; w < kW; ++w) {
-                gs[kW - 1 - w] = mine;
-                mine = apply2(r[w], mine);
-            }
-#pragma unroll
-            for (int w = 0; w < kW; ++w) {
-                s.maps[buf][w][lane] = make_float4(hs.x, hs.y, gs[w].x, gs[w].y);
-                hs = apply2(m[w], hs);
-            }
+            for (int w = 0; w < kW; ++w) reinterpret_cast<float2 *>(&s.maps[buf][w][lane])[1] = e[kW - 1 - w];
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.ready[buf]);
             if ((t.flags & 2) && rank == 0) {
