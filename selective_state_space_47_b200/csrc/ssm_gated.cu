@@ -387,16 +387,17 @@ __device__ __forceinline__ void copy_async_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-template <Load LOAD>
-constexpr int kLoaders = LOAD == kTma ? 1 : 3;  // loading warps
+// Loading warps. Three keep up with tiles that are fetched in small pieces; the backward in bfloat16 has one, for
+// the registers of its other warps (96 instead of 80: B=4 L=4096 D=2054 282 -> 205 us).
+template <Load LOAD, bool BWD = false, int SIZE = 0>
+constexpr int kLoaders = LOAD == kTma || (LOAD == kAsync && BWD && SIZE == 2) ? 1 : 3;
 
 // Rows w, w + NL, ... of a tile of one tensor, by one of the loading warps; zeros past the
 // last step and the last channel, as TMA fills them. PAIRS: a lane's two channels lie on
 // their own size; else channels lane and lane + 32 come one by one.
-template <typename T, int ROWS, Load LOAD>
+template <typename T, int ROWS, Load LOAD, int NL>
 __device__ __forceinline__ void load_rows(T (*dst)[64], const T *base, const int64_t at, const int64_t stride, const int steps, const int64_t width,
                                           const bool pairs, const int w, const int lane) {
-    constexpr int NL = kLoaders<LOAD>;
     const T *src = base + at;
     if constexpr (LOAD == kAsync) {
         if (pairs) {
@@ -539,9 +540,9 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, 2)
             } else {
                 const int w = warp - kW - 1, steps = int(max(int64_t(0), min(int64_t(ROWS), p.s.L - t0)));
                 const int64_t d = int64_t(g) * 64, width = p.s.D - d;
-                load_rows<T, ROWS, LOAD>(s.stage[st][0], p.x, b * p.xb + t0 * p.xt + d, p.xt, steps, width, pairs, w, lane);
-                load_rows<T, ROWS, LOAD>(s.stage[st][1], p.r, b * p.rb + t0 * p.rt + d, p.rt, steps, width, pairs, w, lane);
-                load_rows<T, ROWS, LOAD>(s.stage[st][2], p.i, b * p.ib + t0 * p.it + d, p.it, steps, width, pairs, w, lane);
+                load_rows<T, ROWS, LOAD, NL>(s.stage[st][0], p.x, b * p.xb + t0 * p.xt + d, p.xt, steps, width, pairs, w, lane);
+                load_rows<T, ROWS, LOAD, NL>(s.stage[st][1], p.r, b * p.rb + t0 * p.rt + d, p.rt, steps, width, pairs, w, lane);
+                load_rows<T, ROWS, LOAD, NL>(s.stage[st][2], p.i, b * p.ib + t0 * p.it + d, p.it, steps, width, pairs, w, lane);
             }
             return tile;
         });
@@ -715,7 +716,7 @@ struct BwdArgs {
 
 template <typename T, int K>
 struct BwdShared {
-    static constexpr int kMaxCluster = 8;
+    static constexpr int kMaxCluster = 16;
     T stage[kStages][4][kW * K][64];  // x, r, i, dy of a tile; then dx, dr, di in the first three
     float4 maps[2][kW][32];           // a warp's map of the state, then its start: h and g of a lane's two channels
     float2 adj[2][kW][32];            // H of its map of the adjoint (P is the same)
@@ -818,9 +819,9 @@ __device__ __forceinline__ float2 bwd_grads_of(const T *x, const T *dy, const fl
 // steps stay in registers between the two passes over them; a tile's tokens stay in
 // its stage until its gradients, written over them, have left.
 template <typename T, int K, Load LOAD>
-__global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, sizeof(T) == 2 ? 2 : 1)
+__global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 32, sizeof(T) == 2 ? 2 : 1)
     gated_bwd_kernel(const BwdArgs<T> p, const __grid_constant__ Maps7 tm, const bool pairs) {
-    constexpr int NL = kLoaders<LOAD>, ROWS = kW * K;
+    constexpr int NL = kLoaders<LOAD, true, sizeof(T)>, ROWS = kW * K;
     static_assert(ROWS == kChunk, "a tile is a chunk");
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     BwdShared<T, K> &s = *reinterpret_cast<BwdShared<T, K> *>(smem_raw);
@@ -855,10 +856,10 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, sizeof(T) == 2
             } else {
                 const int w = warp - kW - 1, steps = int(max(int64_t(0), min(int64_t(ROWS), p.s.L - t0)));
                 const int64_t d = int64_t(g) * 64, width = p.s.D - d;
-                load_rows<T, ROWS, LOAD>(s.stage[st][0], p.x, b * p.xb + t0 * p.xt + d, p.xt, steps, width, pairs, w, lane);
-                load_rows<T, ROWS, LOAD>(s.stage[st][1], p.r, b * p.rb + t0 * p.rt + d, p.rt, steps, width, pairs, w, lane);
-                load_rows<T, ROWS, LOAD>(s.stage[st][2], p.i, b * p.ib + t0 * p.it + d, p.it, steps, width, pairs, w, lane);
-                load_rows<T, ROWS, LOAD>(s.stage[st][3], p.dy, (int64_t(b) * p.s.L + t0) * p.s.D + d, p.s.D, steps, width, pairs, w, lane);
+                load_rows<T, ROWS, LOAD, NL>(s.stage[st][0], p.x, b * p.xb + t0 * p.xt + d, p.xt, steps, width, pairs, w, lane);
+                load_rows<T, ROWS, LOAD, NL>(s.stage[st][1], p.r, b * p.rb + t0 * p.rt + d, p.rt, steps, width, pairs, w, lane);
+                load_rows<T, ROWS, LOAD, NL>(s.stage[st][2], p.i, b * p.ib + t0 * p.it + d, p.it, steps, width, pairs, w, lane);
+                load_rows<T, ROWS, LOAD, NL>(s.stage[st][3], p.dy, (int64_t(b) * p.s.L + t0) * p.s.D + d, p.s.D, steps, width, pairs, w, lane);
             }
             return tile;
         });
@@ -1264,7 +1265,7 @@ template <typename T, int K, Load LOAD>
 ssm_status launch_bwd(BwdArgs<T> p, const Maps7 &tm, bool pairs, float *dlam, cudaStream_t st) {
     static Residency resident;
     constexpr size_t smem = sizeof(BwdShared<T, K>);
-    constexpr int threads = (kW + 1 + kLoaders<LOAD>) * 32;
+    constexpr int threads = (kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 32;
     const auto kernel = gated_bwd_kernel<T, K, LOAD>;
     const int64_t columns = p.s.B * p.s.groups, n = p.s.B * p.s.D;
     const int segs = max_segs(columns, ceil_div(p.s.L, kChunk));
