@@ -477,14 +477,13 @@ class _Launch:
     __slots__ = ("handle", "contexts")
 
     def __init__(self, dev, stream, tensors):
-        self.contexts = ()
+        index = dev.index
         if stream is None:
-            if torch.cuda.current_device() != dev.index:
-                self.contexts = (torch.cuda.device(dev),)
-            self.handle = _raw_stream(dev.index)
+            self.contexts = () if torch.cuda.current_device() == index else (torch.cuda.device(dev),)
+            self.handle = _raw_stream(index)
         else:
             self.handle = _resolve_stream(stream, dev).cuda_stream
-            if self.handle != _raw_stream(dev.index):
+            if self.handle != _raw_stream(index):
                 for t in tensors:
                     if t is not None:
                         t.record_stream(stream)
@@ -505,28 +504,21 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _check(t, name, shape, dtype, device):
-    """_need, quick where nothing is wrong."""
-    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.is_cuda and t.device == device
-            and t.is_contiguous()):
-        _need(t, name, shape, dtype, device)
+def _check(t, name, shape, dtype, index):
+    """_need on CUDA device `index`, quick where nothing is wrong."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.is_cuda
+            and t.get_device() == index and t.is_contiguous()):
+        _need(t, name, shape, dtype, torch.device("cuda", max(index, 0)))
 
 
-def _check_strided(t, name, shape, dtype, device):
+def _check_strided(t, name, shape, dtype, index):
     """As _check, for tokens [.., D] whose channels are neighbours in memory but whose leading
-    dimensions may have any stride; returns those strides (0 where the size is 1)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name}: must be on {device} (a CUDA device)")
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1:
+    dimensions may have any stride."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.is_cuda
+            and t.get_device() == index):
+        _need(t, name, shape, dtype, torch.device("cuda", max(index, 0)))
+    if t.stride(-1) != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the channels must be contiguous (stride 1 in the last dimension)")
-    return tuple(v if n > 1 else 0 for v, n in zip(st[:-1], shape))
 
 
 def _scratch(nbytes, workspace, dev):
@@ -543,21 +535,22 @@ def _scratch(nbytes, workspace, dev):
 
 def _gated_head(x, r, i, lam, reset, c, h0):
     """Check what the gated scan's forward and backward take alike: the argument structs' first fields."""
-    dev, tok = x.device, x.dtype
+    index, tok, shape = x.get_device(), x.dtype, x.shape
     if tok not in _TOKEN_DTYPES:
         raise TypeError(f"x: dtype must be float32 or bfloat16, got {tok}")
-    if x.dim() != 3:
+    if len(shape) != 3:
         raise ValueError("x must be [B, L, D]")
-    shape = x.shape
     Bsz, L, Dm = shape
-    sx, sr, si = (_check_strided(t, name, shape, tok, dev) for t, name in ((x, "x"), (r, "r"), (i, "i")))
-    _check(lam, "lam", (Dm,), torch.float32, dev)
+    _check_strided(x, "x", shape, tok, index)
+    _check_strided(r, "r", shape, tok, index)
+    _check_strided(i, "i", shape, tok, index)
+    _check(lam, "lam", (Dm,), torch.float32, index)
     if reset is not None:
-        _check(reset, "reset", (Bsz, L), torch.bool, dev)
+        _check(reset, "reset", (Bsz, L), torch.bool, index)
     if h0 is not None:
-        _check(h0, "h0", (Bsz, Dm), torch.float32, dev)
-    return (Bsz, L, Dm, _TOKEN_DTYPES[tok], 0, c, x.data_ptr(), r.data_ptr(), i.data_ptr(), sx, sr, si, _at(reset),
-            lam.data_ptr())
+        _check(h0, "h0", (Bsz, Dm), torch.float32, index)
+    return (Bsz, L, Dm, _TOKEN_DTYPES[tok], 0, c, x.data_ptr(), r.data_ptr(), i.data_ptr(), x.stride()[:2], r.stride()[:2],
+            i.stride()[:2], _at(reset), lam.data_ptr())
 
 
 def _gated_states(Bsz, L, Dm, dev):
@@ -587,13 +580,13 @@ def gated_scan_fwd(x, r, i, lam, h0=None, *, reset=None, c=8.0, return_last_stat
     """
     head = _gated_head(x, r, i, lam, reset, c, h0)
     Bsz, L, Dm = x.shape
-    dev, tok = x.device, x.dtype
+    dev, tok, index = x.device, x.dtype, x.get_device()
     with _Launch(dev, stream, (x, r, i, lam, reset, h0, out, h_last)) as handle:
         y = torch.empty((Bsz, L, Dm), dtype=tok, device=dev) if out is None else out
         if out is not None:
-            _check(y, "out", (Bsz, L, Dm), tok, dev)
+            _check(y, "out", (Bsz, L, Dm), tok, index)
         if h_last is not None:
-            _check(h_last, "h_last", (Bsz, Dm), torch.float32, dev)
+            _check(h_last, "h_last", (Bsz, Dm), torch.float32, index)
         elif return_last_state:
             h_last = torch.empty((Bsz, Dm), dtype=torch.float32, device=dev)
         states = _gated_states(Bsz, L, Dm, dev) if return_states else None
@@ -614,15 +607,15 @@ def gated_scan_bwd(x, r, i, lam, dy, h0=None, dh_last=None, *, states=None, rese
     """
     head = _gated_head(x, r, i, lam, reset, c, h0)
     shape = Bsz, L, Dm = x.shape
-    dev, tok = x.device, x.dtype
-    _check(dy, "dy", shape, tok, dev)
+    dev, tok, index = x.device, x.dtype, x.get_device()
+    _check(dy, "dy", shape, tok, index)
     if dh_last is not None:
-        _check(dh_last, "dh_last", (Bsz, Dm), torch.float32, dev)
+        _check(dh_last, "dh_last", (Bsz, Dm), torch.float32, index)
     with _Launch(dev, stream, (x, r, i, lam, reset, h0, dy, dh_last, states)) as handle:
         if states is None:
             states = _gated_states(Bsz, L, Dm, dev)
             _gated_fwd(head, h0, None, None, states, None, dev, handle)
-        _check(states, "states", (Bsz, -(-L // _native.SSM_GATED_CHUNK), Dm), torch.float32, dev)
+        _check(states, "states", (Bsz, -(-L // _native.SSM_GATED_CHUNK), Dm), torch.float32, index)
         dx, dr, di, dlam, dh0 = _gated_bwd(head, x, states, dy, dh_last, workspace, handle)
     return dict(dx=dx, dr=dr, di=di, dlam=dlam, dh0=dh0)
 
@@ -654,19 +647,22 @@ def gated_step(x, r, i, lam, h, *, c=8.0, h_out=None, out=None, stream=None):
     if len(shape) != 2:
         raise ValueError("x must be [B, D]")
     Bsz, Dm = shape
-    sx, sr, si = (_check_strided(t, name, shape, tok, dev)[0] for t, name in ((x, "x"), (r, "r"), (i, "i")))
-    _check(lam, "lam", (Dm,), torch.float32, dev)
-    _check(h, "h", shape, torch.float32, dev)
+    index = x.get_device()
+    _check_strided(x, "x", shape, tok, index)
+    _check_strided(r, "r", shape, tok, index)
+    _check_strided(i, "i", shape, tok, index)
+    _check(lam, "lam", (Dm,), torch.float32, index)
+    _check(h, "h", shape, torch.float32, index)
     if h_out is None:
         h_out = h
     else:
-        _check(h_out, "h_out", shape, torch.float32, dev)
+        _check(h_out, "h_out", shape, torch.float32, index)
     with _Launch(dev, stream, (x, r, i, lam, h, h_out, out)) as handle:
         y = torch.empty((Bsz, Dm), dtype=tok, device=dev) if out is None else out
         if out is not None:
-            _check(y, "out", shape, tok, dev)
-        rc = _native.lib().ssm_gated_step(Bsz, Dm, _TOKEN_DTYPES[tok], c, x.data_ptr(), sx, r.data_ptr(), sr, i.data_ptr(),
-                                          si, lam.data_ptr(), h.data_ptr(), h_out.data_ptr(), y.data_ptr(), handle)
+            _check(y, "out", shape, tok, index)
+        rc = _native.lib().ssm_gated_step(Bsz, Dm, _TOKEN_DTYPES[tok], c, x.data_ptr(), x.stride(0), r.data_ptr(), r.stride(0),
+                                          i.data_ptr(), i.stride(0), lam.data_ptr(), h.data_ptr(), h_out.data_ptr(), y.data_ptr(), handle)
     _native.check(rc, "ssm_gated_step")
     return y
 
@@ -728,23 +724,23 @@ def layer_norm_fwd(x, weight, bias=None, residual=None, *, eps=1e-5, out=None, r
     residual in float32 (residual_out, which may be residual itself); with return_stats also the
     rows' mean and 1 / sqrt(var + eps), float32.
     """
-    dev, tok, shape = x.device, x.dtype, x.shape
+    dev, tok, shape, index = x.device, x.dtype, x.shape, x.get_device()
     rows, Dm = _norm_shape(x, "x")
     f32 = torch.float32
-    _check(x, "x", shape, tok, dev)
-    _check(weight, "weight", (Dm,), f32, dev)
+    _check(x, "x", shape, tok, index)
+    _check(weight, "weight", (Dm,), f32, index)
     if bias is not None:
-        _check(bias, "bias", (Dm,), f32, dev)
+        _check(bias, "bias", (Dm,), f32, index)
     if residual is not None:
-        _check(residual, "residual", shape, f32, dev)
+        _check(residual, "residual", shape, f32, index)
     elif residual_out is not None:
         raise ValueError("residual_out needs residual")
     with _Launch(dev, stream, (x, weight, bias, residual, out, residual_out)) as handle:
         y = torch.empty(shape, dtype=tok, device=dev) if out is None else out
         if out is not None:
-            _check(y, "out", shape, tok, dev)
+            _check(y, "out", shape, tok, index)
         if residual_out is not None:
-            _check(residual_out, "residual_out", shape, f32, dev)
+            _check(residual_out, "residual_out", shape, f32, index)
         elif residual is not None:
             residual_out = torch.empty(shape, dtype=f32, device=dev)
         mean, rstd = (torch.empty(shape[:-1], dtype=f32, device=dev) for _ in range(2)) if return_stats else (None, None)
@@ -765,18 +761,18 @@ def layer_norm_bwd(dy, s, weight, mean, rstd, dresidual_out=None, *, residual=Fa
     Returns a dict: dx in dy's dtype; dweight and (None without bias) dbias [D] float32;
     with residual dresidual in float32 (dx itself for float32 tokens), else None.
     """
-    dev, tok, shape = dy.device, dy.dtype, dy.shape
+    dev, tok, shape, index = dy.device, dy.dtype, dy.shape, dy.get_device()
     rows, Dm = _norm_shape(dy, "dy")
     f32 = torch.float32
-    _check(dy, "dy", shape, tok, dev)
-    _check(s, "s", shape, f32 if residual else tok, dev)
-    _check(weight, "weight", (Dm,), f32, dev)
-    _check(mean, "mean", shape[:-1], f32, dev)
-    _check(rstd, "rstd", shape[:-1], f32, dev)
+    _check(dy, "dy", shape, tok, index)
+    _check(s, "s", shape, f32 if residual else tok, index)
+    _check(weight, "weight", (Dm,), f32, index)
+    _check(mean, "mean", shape[:-1], f32, index)
+    _check(rstd, "rstd", shape[:-1], f32, index)
     if dresidual_out is not None:
         if not residual:
             raise ValueError("dresidual_out needs residual")
-        _check(dresidual_out, "dresidual_out", shape, f32, dev)
+        _check(dresidual_out, "dresidual_out", shape, f32, index)
     with _Launch(dev, stream, (dy, s, weight, mean, rstd, dresidual_out)) as handle:
         dx, dweight, dbias, dres = _norm_bwd(rows, Dm, dy, s, weight, mean, rstd, dresidual_out, residual, bias, workspace, handle)
     return dict(dx=dx, dweight=dweight, dbias=dbias, dresidual=dres)

@@ -4,11 +4,19 @@
 //   w_t = p sigmoid(r_t), p = c softplus(lam);  a_t = exp(-w_t);  beta_t = sqrt(1 - a_t^2)
 //   h_t = a_t h_{t-1} + beta_t sigmoid(i_t) x_t,  y_t = h_t;  at a reset a_t = 0, beta_t = 1
 //
-// A tile is 32 V channels by W K steps: lane = V neighbouring channels, warp = K
-// consecutive steps, held in registers. A piece of time acts on the state entering it as
-// h -> P h + H, and two such maps compose, so each thread forms the map of its K steps,
-// the warps of a block chain theirs through shared memory, and the tiles chain theirs
-// through the workspace.
+// A piece of time acts on the state entering it as h -> P h + H, and two such maps compose. A
+// column is 64 channels of one sequence, a tile 8 K steps of it: lane = two neighbouring
+// channels, warp = K steps, in registers from the one read of the tokens to the one write of
+// the results. Each warp forms the map of its steps, a block composes its tile's, and a
+// cluster of blocks, which walks the column, exchanges its tiles' maps through shared memory. So time is
+// passed over once, the state between rounds never leaves the chip, and the order in which pieces are
+// joined depends on the shape alone.
+//
+// What bounds it (B=1 L=65536 D=5120 bfloat16): the forward takes 0.61 ms, 4.4 TB/s of 6.5, with the issue slots at 50%
+// and the special-function unit (four operations an element, 16 a clock) at 52%; the
+// same kernel with the sigmoids left out takes 0.48 ms. The backward takes 1.27 ms, 3.7 TB/s, at 68 instructions and five
+// special-function operations an element. float32, with twice the bytes to the same arithmetic, moves 6.3 TB/s forward and
+// 5.2 TB/s backward (B=8 L=4096 D=2048).
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <float.h>
@@ -26,7 +34,7 @@ using namespace ssm;
 namespace {
 
 constexpr int kChunk = SSM_GATED_CHUNK;  // steps between the states kept for the backward
-constexpr int kW = 8;                    // warps of a block
+constexpr int kW = 8;                    // computing warps of a block
 constexpr size_t kWsHeader = 256;
 
 // ------------------------------------------------------------- element math
@@ -107,7 +115,7 @@ __device__ __forceinline__ void stv(T *p, const Vec<T, V> v) {
 
 struct Shape {
     int64_t B, L, D;
-    int64_t groups, tiles;  // channel groups of 32 V, tiles of time
+    int64_t groups;  // of 64 channels
     float c;
 };
 
@@ -233,9 +241,8 @@ __device__ __noinline__ void wait_landed(uint64_t *bar, uint32_t parity) {
 }
 
 // ------------------------------------------------------------------- forward
-constexpr int kItemSlots = 8;
-constexpr int kInfos = 4;
-constexpr int kStages = 2;
+constexpr int kItemSlots = 16;  // of items told of, and of tiles' particulars: more than any warp of a
+constexpr int kInfos = 8;       // cluster is ahead of another
 
 // How a call's time is dealt out. A column (64 channels of one sequence) is walked by a cluster
 // of `cluster` blocks, which take neighbouring tiles of W K steps at a time; an item is a
@@ -269,9 +276,10 @@ struct TileInfo {
     int flags;  // 1: first of its item, 2: last of its item
 };
 
-template <typename T, int K>
+template <typename T, int K, bool LAG>
 struct FwdShared {
-    static constexpr int kMaxCluster = sizeof(T) * K <= 16 ? 16 : 8;
+    static constexpr int kStages = LAG ? 3 : 2;
+    static constexpr int kMaxCluster = LAG || sizeof(T) * K <= 16 ? 16 : 8;  // (two blocks fit an SM without LAG)
     T stage[kStages][3][kW * K][64];       // x, r, i of a tile
     float4 maps[2][kW][32];                // a warp's map (P, H of a lane's two channels), then its start
     float4 inbox[2][kMaxCluster][32];      // the blocks' maps of a round, from the whole cluster
@@ -285,6 +293,8 @@ struct FwdShared {
 struct Maps3 {
     CUtensorMap x, r, i;
 };
+
+constexpr int kFewColumns = 24;  // up to here LAG: 1536 channels of one sequence (575 against 496 us at L=131072)
 
 enum Load { kTma, kAsync, kPlain };  // 16-byte rows; pieces of 4 or 8 bytes; elements of 2 bytes
 
@@ -442,6 +452,7 @@ __device__ __forceinline__ void load_rows(T (*dst)[64], const T *base, const int
 template <Load LOAD, typename Args, typename Shared, typename Issue>
 __device__ __forceinline__ void load_tiles(const Args &p, Shared &s, const int w, const int lane, const uint32_t rank, const unsigned int C,
                                            const unsigned int columns, const unsigned int groups, const bool counted, const Issue &issue) {
+    constexpr int kStages = Shared::kStages;
     unsigned int it = 0;
     for (unsigned int q = 0;; ++q) {
         const int slot = q % kItemSlots;
@@ -503,13 +514,17 @@ __device__ __forceinline__ void load_tiles(const Args &p, Shared &s, const int w
 // Segments of a column are handed out in the order of time by a counter; a segment starts from
 // the state that its predecessor leaves in the workspace, which with more columns than clusters is
 // there long before (and after a local pass is always there).
-template <typename T, int K, Load LOAD>
-__global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, 2)
+// LAG: a tile's outputs are written one round late, once the next tile's steps are in registers too; by then its
+// start is there, and no warp waits for the way to the cluster and back. That takes the registers of a whole SM per
+// block. It pays where there are too few columns for two blocks an SM anyway (B=1 L=131072 D=1024: 481 -> 340 us, D=512 263 -> 189 us);
+// with enough of them the other block fills the wait (D=2048: 587 us without, 707 with).
+template <typename T, int K, Load LOAD, bool LAG>
+__global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, LAG ? 1 : 2)
     gated_fwd_kernel(const FwdArgs<T> p, const __grid_constant__ Maps3 tm, const bool pairs) {
     static_assert(kChunk % K == 0, "a chunk starts at a warp's first step");
-    constexpr int NL = kLoaders<LOAD>, ROWS = kW * K;
+    constexpr int NL = kLoaders<LOAD>, ROWS = kW * K, kStages = FwdShared<T, K, LAG>::kStages;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    FwdShared<T, K> &s = *reinterpret_cast<FwdShared<T, K> *>(smem_raw);
+    FwdShared<T, K, LAG> &s = *reinterpret_cast<FwdShared<T, K, LAG> *>(smem_raw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned int groups = unsigned(p.s.groups), columns = unsigned(p.pl.columns), C = unsigned(p.pl.cluster);
     const uint32_t rank = cluster_rank();
@@ -618,35 +633,43 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, 2)
         }
     } else {
         // ---------------------------------------------------------- computing
-        for (unsigned int it = 0;; ++it) {
-            const int st = it % kStages, buf = it & 1;
+        // read: tile `it` into decays, inputs and resets, and its map posted; write: its outputs.
+        const auto read = [&](const unsigned int it, float2(&a)[K], float2(&h)[K], unsigned int &fresh) -> bool {
+            const int st = it % kStages;
             const bool ok = wait_phase(&s.full[st], (it / kStages) & 1, &s.abort, p.status);
-            if (!__all_sync(0xffffffffu, ok)) break;
+            if (!__all_sync(0xffffffffu, ok)) return false;
             const TileInfo t = s.tile[it % kInfos];
-            if (t.tile < 0) break;
-            const unsigned int b = t.col / groups;
-            const int64_t d = int64_t(t.col % groups) * 64 + lane * 2, o = int64_t(b) * p.s.D + d;
-            const int64_t t0 = int64_t(t.tile) * ROWS + warp * K;
-            const int steps = int(max(int64_t(0), min(int64_t(K), p.s.L - t0)));
-            unsigned int fresh = 0;
-            if (p.reset) fresh = __ballot_sync(0xffffffffu, lane < steps && p.reset[int64_t(b) * p.s.L + t0 + lane] != 0);
+            if (t.tile < 0) return false;
+            fresh = 0;
+            if (p.reset) {
+                const int64_t tl = int64_t(t.tile) * ROWS + warp * K + lane;
+                fresh = __ballot_sync(0xffffffffu, lane < K && tl < p.s.L && p.reset[int64_t(t.col / groups) * p.s.L + tl] != 0);
+            }
             const float2 rt = *reinterpret_cast<const float2 *>(&s.rate[st][lane * 2]);
             const T *x = &s.stage[st][0][warp * K][lane * 2], *r = &s.stage[st][1][warp * K][lane * 2],
                     *i = &s.stage[st][2][warp * K][lane * 2];
-            float2 a[K], h[K];
             float4 m;
             float big = 1e30f;
-            if (fresh == 0 && __all_sync(0xffffffffu, fmaxf(rt.x, rt.y) < 0.5f && fminf(rt.x, rt.y) > 1e-18f)) m = fwd_steps_of<T, K, true>(x, r, i, rt, fresh, a, h, big);
+            if (fresh == 0 && __all_sync(0xffffffffu, fmaxf(rt.x, rt.y) < 0.5f && fminf(rt.x, rt.y) > 1e-18f))
+                m = fwd_steps_of<T, K, true>(x, r, i, rt, fresh, a, h, big);
             if (__any_sync(0xffffffffu, big > 60.0f)) m = fwd_steps_of<T, K, false>(x, r, i, rt, fresh, a, h, big);
-            s.maps[buf][warp][lane] = m;
+            s.maps[it & 1][warp][lane] = m;
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&s.posted[buf]);
+                mbar_arrive(&s.posted[it & 1]);
                 mbar_arrive(&s.empty[st]);
             }
-            wait_phase(&s.ready[buf], (it >> 1) & 1, &s.abort, p.status);
+            return true;
+        };
+        const auto write = [&](const unsigned int it, const float2(&a)[K], const float2(&h)[K], const unsigned int fresh) {
+            wait_phase(&s.ready[it & 1], (it >> 1) & 1, &s.abort, p.status);
+            const TileInfo t = s.tile[it % kInfos];
+            const unsigned int b = t.col / groups;
+            const int64_t d = int64_t(t.col % groups) * 64 + lane * 2;
+            const int64_t t0 = int64_t(t.tile) * ROWS + warp * K;
+            const int steps = int(max(int64_t(0), min(int64_t(K), p.s.L - t0)));
             if (!p.maps && d < p.s.D && steps > 0) {
-                float2 hs = *reinterpret_cast<const float2 *>(&s.maps[buf][warp][lane]);
+                float2 hs = *reinterpret_cast<const float2 *>(&s.maps[it & 1][warp][lane]);
                 const bool both = d + 1 < p.s.D;
                 if (p.states && t0 % kChunk == 0) {
                     float *q = p.states + (int64_t(b) * ((p.s.L + kChunk - 1) / kChunk) + t0 / kChunk) * p.s.D + d;
@@ -674,11 +697,27 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, 2)
                         }
                 }
                 if (p.h_last && t0 + steps == p.s.L) {
-                    p.h_last[o] = hs.x;
-                    if (both) p.h_last[o + 1] = hs.y;
+                    p.h_last[int64_t(b) * p.s.D + d] = hs.x;
+                    if (both) p.h_last[int64_t(b) * p.s.D + d + 1] = hs.y;
                 }
             }
             __syncwarp();
+        };
+        float2 a0[K], h0[K];
+        unsigned int f0 = 0;
+        if constexpr (LAG) {
+            float2 a1[K], h1[K];
+            unsigned int f1 = 0;
+            bool more = read(0, a0, h0, f0);
+            for (unsigned int it = 0; more; it += 2) {
+                const bool next = read(it + 1, a1, h1, f1);
+                write(it, a0, h0, f0);
+                if (!next) break;
+                more = read(it + 2, a0, h0, f0);
+                write(it + 1, a1, h1, f1);
+            }
+        } else {
+            for (unsigned int it = 0; read(it, a0, h0, f0); ++it) write(it, a0, h0, f0);
         }
     }
     __syncwarp();
@@ -716,6 +755,7 @@ struct BwdArgs {
 
 template <typename T, int K>
 struct BwdShared {
+    static constexpr int kStages = 2;
     static constexpr int kMaxCluster = 16;
     T stage[kStages][4][kW * K][64];  // x, r, i, dy of a tile; then dx, dr, di in the first three
     float4 maps[2][kW][32];           // a warp's map of the state, then its start: h and g of a lane's two channels
@@ -821,7 +861,7 @@ __device__ __forceinline__ float2 bwd_grads_of(const T *x, const T *dy, const fl
 template <typename T, int K, Load LOAD>
 __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 32, sizeof(T) == 2 ? 2 : 1)
     gated_bwd_kernel(const BwdArgs<T> p, const __grid_constant__ Maps7 tm, const bool pairs) {
-    constexpr int NL = kLoaders<LOAD, true, sizeof(T)>, ROWS = kW * K;
+    constexpr int NL = kLoaders<LOAD, true, sizeof(T)>, ROWS = kW * K, kStages = BwdShared<T, K>::kStages;
     static_assert(ROWS == kChunk, "a tile is a chunk");
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     BwdShared<T, K> &s = *reinterpret_cast<BwdShared<T, K> *>(smem_raw);
@@ -1095,9 +1135,6 @@ bool sizes_fit(int64_t B, int64_t L, int64_t D, int64_t t) {
     return B * ceil_div(L, t) * ceil_div(D, 32) <= INT_MAX;
 }
 
-struct Strides {
-    int64_t b, t;
-};
 bool even(const int64_t *s) { return s[0] % 2 == 0 && s[1] % 2 == 0; }
 
 ssm_status launched() { return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_ERR_CUDA; }
@@ -1130,8 +1167,10 @@ int clusters_resident(Residency &r, const void *kernel, int threads, size_t smem
         cfg.attrs = &at, cfg.numAttrs = 1;
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess ||
             cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0)
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n <= 0) {
+            cudaGetLastError();  // not left for the next call to find
             return 0;
+        }
         r.n[dev][log2c].store(n, std::memory_order_relaxed);
     }
     return n;
@@ -1150,7 +1189,8 @@ bool make_plan(Plan &pl, Residency &r, const void *kernel, int threads, size_t s
         const int c = 1 << k;
         if (c > 1 && c / 2 >= tiles) break;
         const int n = clusters_resident(r, kernel, threads, smem, k);
-        if (n <= 0) return false;
+        if (n <= 0 && k == 0) return false;
+        if (n <= 0) break;  // a size this GPU does not take
         const int64_t rounds = ceil_div(tiles, c);
         const auto consider = [&](int64_t iters, bool local, double cost) {
             if (cost >= best) return;
@@ -1171,15 +1211,15 @@ bool make_plan(Plan &pl, Residency &r, const void *kernel, int threads, size_t s
     return true;
 }
 
-template <typename T, int K, Load LOAD>
+template <typename T, int K, Load LOAD, bool LAG>
 ssm_status launch_fwd(FwdArgs<T> p, const Maps3 &tm, bool pairs, cudaStream_t st) {
     static Residency resident;
-    constexpr size_t smem = sizeof(FwdShared<T, K>);
+    constexpr size_t smem = sizeof(FwdShared<T, K, LAG>);
     constexpr int threads = (kW + 1 + kLoaders<LOAD>) * 32;
-    const auto kernel = gated_fwd_kernel<T, K, LOAD>;
+    const auto kernel = gated_fwd_kernel<T, K, LOAD, LAG>;
     const int64_t columns = p.s.B * p.s.groups, n = p.s.B * p.s.D;
     const int segs = max_segs(columns, ceil_div(p.s.L, kChunk));
-    if (!make_plan(p.pl, resident, reinterpret_cast<const void *>(kernel), threads, smem, FwdShared<T, K>::kMaxCluster, columns,
+    if (!make_plan(p.pl, resident, reinterpret_cast<const void *>(kernel), threads, smem, FwdShared<T, K, LAG>::kMaxCluster, columns,
                    ceil_div(p.s.L, kW * K), segs))
         return SSM_ERR_CUDA;
     unsigned char *ws = reinterpret_cast<unsigned char *>(p.counter);
@@ -1196,11 +1236,11 @@ ssm_status launch_fwd(FwdArgs<T> p, const Maps3 &tm, bool pairs, cudaStream_t st
     cfg.attrs = &at, cfg.numAttrs = 1;
     if (p.pl.local) {
         p.maps = maps;
-        if (cudaLaunchKernelEx(&cfg, kernel, p, tm, pairs) != cudaSuccess) return SSM_ERR_CUDA;
+        if (cudaLaunchKernelEx(&cfg, kernel, p, tm, pairs) != cudaSuccess) return launched();
         p.maps = nullptr;
         gated_starts_kernel<<<unsigned(ceil_div(n, 128)), 128, 0, st>>>(n, p.pl.segs, p.h0, maps, p.starts);
     }
-    if (cudaLaunchKernelEx(&cfg, kernel, p, tm, pairs) != cudaSuccess) return SSM_ERR_CUDA;
+    cudaLaunchKernelEx(&cfg, kernel, p, tm, pairs);
     return launched();
 }
 
@@ -1239,7 +1279,7 @@ template <typename T>
 ssm_status run_fwd(const ssm_gated_args *a, cudaStream_t st) {
     constexpr size_t es = sizeof(T);
     FwdArgs<T> p = {};
-    p.s = {a->batch, a->seqlen, a->dim, ceil_div(a->dim, 64), 0, a->c};
+    p.s = {a->batch, a->seqlen, a->dim, ceil_div(a->dim, 64), a->c};
     p.counter = static_cast<unsigned int *>(a->workspace);
     p.x = static_cast<const T *>(a->x), p.r = static_cast<const T *>(a->r), p.i = static_cast<const T *>(a->i);
     p.xb = a->x_stride[0], p.xt = a->x_stride[1], p.rb = a->r_stride[0], p.rt = a->r_stride[1];
@@ -1253,11 +1293,13 @@ ssm_status run_fwd(const ssm_gated_args *a, cudaStream_t st) {
                token_map(&tm.r, a->r, a->dtype, a->batch, a->seqlen, a->dim, a->r_stride, rows) &&
                token_map(&tm.i, a->i, a->dtype, a->batch, a->seqlen, a->dim, a->i_stride, rows);
     };
-    constexpr int K = es == 2 ? 16 : 8;  // stages of 48 KB; half of it where the loading warps are what counts
+    // Stages of 48 KB, of 24 KB where the loading warps are what counts.
+    constexpr int K = es == 2 ? 16 : 8;
+    const bool few = p.s.B * p.s.groups <= kFewColumns;
     Maps3 tm = {};
-    if (maps_of(tm, kW * K)) return launch_fwd<T, K, kTma>(p, tm, pairs, st);
-    if (pairs || es == 4) return launch_fwd<T, K / 2, kAsync>(p, tm, pairs, st);
-    if constexpr (es == 2) return launch_fwd<T, K / 2, kPlain>(p, tm, pairs, st);
+    if (maps_of(tm, kW * K)) return few ? launch_fwd<T, K, kTma, true>(p, tm, pairs, st) : launch_fwd<T, K, kTma, false>(p, tm, pairs, st);
+    if (pairs || es == 4) return few ? launch_fwd<T, K, kAsync, true>(p, tm, pairs, st) : launch_fwd<T, K / 2, kAsync, false>(p, tm, pairs, st);
+    if constexpr (es == 2) return launch_fwd<T, K / 2, kPlain, false>(p, tm, pairs, st);
     return SSM_ERR_UNSUPPORTED;
 }
 
@@ -1287,11 +1329,11 @@ ssm_status launch_bwd(BwdArgs<T> p, const Maps7 &tm, bool pairs, float *dlam, cu
     cfg.attrs = &at, cfg.numAttrs = 1;
     if (p.pl.local) {
         p.maps = maps;
-        if (cudaLaunchKernelEx(&cfg, kernel, p, tm, pairs) != cudaSuccess) return SSM_ERR_CUDA;
+        if (cudaLaunchKernelEx(&cfg, kernel, p, tm, pairs) != cudaSuccess) return launched();
         p.maps = nullptr;
         gated_starts_kernel<<<unsigned(ceil_div(n, 128)), 128, 0, st>>>(n, p.pl.segs, p.dh_last, maps, p.starts);
     }
-    if (cudaLaunchKernelEx(&cfg, kernel, p, tm, pairs) != cudaSuccess) return SSM_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, p, tm, pairs) != cudaSuccess) return launched();
     gated_dlam_kernel<<<unsigned(ceil_div(p.s.D, 32)), 1024, 0, st>>>(int64_t(p.pl.segs) * p.pl.cluster * kW * p.s.B, p.s.D, p.s.c, p.parts,
                                                                       p.lam, dlam);
     return launched();
@@ -1301,7 +1343,7 @@ template <typename T>
 ssm_status run_bwd(const ssm_gated_bwd_args *a, cudaStream_t st) {
     constexpr size_t es = sizeof(T);
     BwdArgs<T> p = {};
-    p.s = {a->batch, a->seqlen, a->dim, ceil_div(a->dim, 64), 0, a->c};
+    p.s = {a->batch, a->seqlen, a->dim, ceil_div(a->dim, 64), a->c};
     p.counter = static_cast<unsigned int *>(a->workspace);
     p.x = static_cast<const T *>(a->x), p.r = static_cast<const T *>(a->r), p.i = static_cast<const T *>(a->i);
     p.dy = static_cast<const T *>(a->dy);
@@ -1345,6 +1387,18 @@ ssm_status check_common(const A *a) {
     return SSM_OK;
 }
 
+// A stride over a single sequence or step is never walked: it counts as 0.
+template <typename A>
+A walked(const A &args) {
+    A a = args;
+    int64_t *const strides[] = {a.x_stride, a.r_stride, a.i_stride};
+    for (int64_t *s : strides) {
+        if (a.batch <= 1) s[0] = 0;
+        if (a.seqlen <= 1) s[1] = 0;
+    }
+    return a;
+}
+
 template <typename A>
 bool strides_fit(const A *a) {
     const int64_t *const strides[] = {a->x_stride, a->r_stride, a->i_stride};
@@ -1371,9 +1425,10 @@ size_t ssm_gated_scan_workspace_size(const ssm_gated_args *a) {
     return (a->batch == 0 || a->dim == 0) ? 0 : carry_bytes(a->batch, a->seqlen, a->dim);
 }
 
-ssm_status ssm_gated_scan_fwd(const ssm_gated_args *a, void *stream) {
-    const ssm_status ok = check_common(a);
+ssm_status ssm_gated_scan_fwd(const ssm_gated_args *args, void *stream) {
+    const ssm_status ok = check_common(args);
     if (ok != SSM_OK) return ok;
+    const ssm_gated_args walk = walked(*args), *a = &walk;
     if (a->batch == 0 || a->dim == 0) return SSM_OK;
     const size_t es = a->dtype == SSM_BF16 ? 2 : 4;
     if (!a->lam || (a->seqlen > 0 && (!a->x || !a->r || !a->i || (!a->y && !a->states && !a->h_last))))
@@ -1405,9 +1460,10 @@ size_t ssm_gated_scan_bwd_workspace_size(const ssm_gated_bwd_args *a) {
            size_t(a->batch) * size_t(a->dim) * size_t(most_parts(columns)) * kW * 4;
 }
 
-ssm_status ssm_gated_scan_bwd(const ssm_gated_bwd_args *a, void *stream) {
-    const ssm_status ok = check_common(a);
+ssm_status ssm_gated_scan_bwd(const ssm_gated_bwd_args *args, void *stream) {
+    const ssm_status ok = check_common(args);
     if (ok != SSM_OK) return ok;
+    const ssm_gated_bwd_args walk = walked(*args), *a = &walk;
     if (a->dim == 0) return SSM_OK;
     const size_t es = a->dtype == SSM_BF16 ? 2 : 4;
     const bool empty = a->batch == 0 || a->seqlen == 0;
@@ -1446,6 +1502,7 @@ ssm_status ssm_gated_step(int64_t batch, int64_t dim, ssm_dtype dtype, float c, 
         return SSM_ERR_INVALID;
     if (!sizes_fit(batch, 1, dim, 1)) return SSM_ERR_UNSUPPORTED;
     if (batch == 0 || dim == 0) return SSM_OK;
+    if (batch == 1) x_stride = r_stride = i_stride = 0;  // never walked
     if (!x || !r || !i || !lam || !h || !h_out || !y) return SSM_ERR_INVALID;
     const size_t es = dtype == SSM_BF16 ? 2 : 4;
     bool two = dim % 2 == 0 && x_stride % 2 == 0 && r_stride % 2 == 0 && i_stride % 2 == 0;

@@ -1,10 +1,13 @@
 """GPU checks of the gated linear recurrence (scan, backward, step) against its float64
 form, elementwise within the bounds derived there."""
+import subprocess
+import sys
+
 import pytest
 import torch
 
 from tests import operators_ref as ref
-from tests.conftest import cuda_available
+from tests.conftest import ROOT, cuda_available
 
 pytestmark = pytest.mark.gpu
 
@@ -61,7 +64,7 @@ def check_bwd(ssm, d, g, dtype, states):
 
 
 SIZES = [(1, 1, 1), (2, 1, 64), (3, 2, 31), (1, 63, 64), (2, 64, 33), (2, 65, 66), (1, 127, 130), (5, 128, 2),
-         (2, 129, 7), (1, 300, 200), (2, 1025, 40), (1, 3000, 10)]
+         (2, 129, 7), (1, 300, 200), (2, 1025, 40), (1, 3000, 10), (2, 70, 8), (1, 200, 16), (300, 5, 24), (1, 65, 264)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
@@ -118,6 +121,88 @@ def test_long_sequences(ssm):
         g = cuda(d)
         _, (_, _, states) = check_fwd(ssm, d, g, dtype)
         check_bwd(ssm, d, g, dtype, states)
+
+
+@pytest.mark.parametrize("B,L,D,dtype", [(1, 6000, 5120, torch.bfloat16), (3, 5000, 1536, torch.bfloat16),
+                                         (4, 3000, 2048, torch.float32), (1, 9001, 1030, torch.bfloat16),
+                                         (1, 50000, 72, torch.bfloat16), (2, 6001, 515, torch.bfloat16),
+                                         (2, 6001, 515, torch.float32)])
+def test_every_way_of_dealing_out_time(ssm, B, L, D, dtype):
+    """More columns than the GPU takes at once (segments handed on in turn), fewer (clusters share a column) and
+    very few (two passes): three channels against the reference, and five runs bit for bit."""
+    gen = torch.Generator(device="cuda").manual_seed(D + L)
+    n = lambda *s: torch.randn(*s, device="cuda", generator=gen)
+    g = {k: n(B, L, D).clamp(-6, 6).to(dtype) for k in ("x", "r", "i", "dy")}
+    g["lam"] = torch.log(torch.expm1(-torch.log(0.9 + 0.099 * torch.rand(D, device="cuda", generator=gen)) / 8.0))
+    g["h0"], g["dh_last"] = n(B, D), n(B, D)
+    g["reset"] = torch.rand(B, L, device="cuda", generator=gen) < 1e-3
+    args, grads = [g[k] for k in FWD], [g[k] for k in ("x", "r", "i", "lam", "dy", "h0", "dh_last")]
+    run = lambda: (ssm.gated_scan_fwd(*args, reset=g["reset"], return_last_state=True, return_states=True))
+    y, h, states = run()
+    got = ssm.gated_scan_bwd(*grads, states=states, reset=g["reset"])
+    for _ in range(4):
+        for a, b in zip((y, h, states), run()):
+            assert torch.equal(a, b)
+        again = ssm.gated_scan_bwd(*grads, states=states, reset=g["reset"])
+        for k in got:
+            assert torch.equal(got[k], again[k]), k
+    sel = torch.tensor([0, D // 2, D - 1], device="cuda")
+    cut = lambda t: t[B - 1:].index_select(t.dim() - 1, sel).cpu()
+    d = {k: cut(v) for k, v in g.items() if k not in ("lam", "reset")}
+    lam, reset = g["lam"][sel].cpu(), g["reset"][B - 1:].cpu()
+    want, bound = ref.gated_scan(d["x"], d["r"], d["i"], lam, d["h0"], reset)
+    ref.check(cut(y), want, bound, dtype, "y")
+    ref.check(cut(h), want[:, -1], bound[:, -1], what="h_last")
+    want, bound = ref.gated_scan_bwd(d["x"], d["r"], d["i"], lam, d["dy"], d["h0"], d["dh_last"], reset)
+    for k in ("dx", "dr", "di", "dh0"):
+        ref.check(cut(got[k]), want[k], bound[k], torch.float32 if k == "dh0" else dtype, k)
+
+
+def test_workspaces(ssm):
+    """A caller's workspace is used, reports its status, and is refused when too small or elsewhere."""
+    d = make(2, 900, 192, torch.bfloat16, seed=51, h0=True)
+    g = cuda(d)
+    args, grads = [g[k] for k in FWD], [g[k] for k in ("x", "r", "i", "lam", "dy", "h0", "dh_last")]
+    want, states = ssm.gated_scan_fwd(*args, return_states=True)
+    ws = ssm.ScanWorkspace()
+    for _ in range(3):
+        assert torch.equal(ssm.gated_scan_fwd(*args, workspace=ws), want)
+        assert ssm.workspace_status(ws) == 0
+        ws.buf.fill_(255)  # what a call finds there does not matter
+        got = ssm.gated_scan_bwd(*grads, states=states, workspace=ws)
+        assert ssm.workspace_status(ws) == 0
+        ws.buf.fill_(255)
+    first = ssm.gated_scan_bwd(*grads, states=states)
+    for k in got:
+        assert torch.equal(got[k], first[k]), k
+    for bad in (torch.empty(64, dtype=torch.uint8, device="cuda"), torch.empty(1 << 24, dtype=torch.uint8)):
+        with pytest.raises(ValueError):
+            ssm.gated_scan_fwd(*args, workspace=bad)
+        with pytest.raises(ValueError):
+            ssm.gated_scan_bwd(*grads, states=states, workspace=bad)
+
+
+def test_first_call_captured():
+    """A process whose first call is made while a graph is captured."""
+    if not cuda_available():
+        pytest.skip("needs a CUDA device")
+    code = """
+import torch, selective_state_space_47_b200 as ssm
+x = torch.randn(2, 500, 64, device="cuda"); lam = torch.zeros(64, device="cuda"); w = torch.ones(64, device="cuda")
+def run():
+    y, st = ssm.gated_scan_fwd(x, x, x, lam, return_states=True)
+    n, m, k = ssm.layer_norm_fwd(y, w, return_stats=True)
+    return [y, n, *ssm.gated_scan_bwd(x, x, x, lam, x, states=st).values(), *ssm.layer_norm_bwd(x, y, w, m, k).values()]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    a = run()
+g.replay()
+b = run()
+torch.cuda.synchronize()
+assert all(p is q is None or torch.equal(p, q) for p, q in zip(a, b))
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT, timeout=120)
 
 
 def test_a_reset_drops_what_came_before(ssm):
