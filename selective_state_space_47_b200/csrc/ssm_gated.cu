@@ -284,6 +284,7 @@ struct FwdShared {
     float4 maps[2][kW][32];                // a warp's map (P, H of a lane's two channels), then its start
     float4 inbox[2][kMaxCluster][32];      // the blocks' maps of a round, from the whole cluster
     float rate[kStages][64];
+    unsigned int fresh[kStages][(kW * K + 31) / 32];
     TileInfo tile[kInfos];
     uint64_t full[kStages], empty[kStages], posted[2], mail[2], ready[2], told[kItemSlots];
     unsigned int item[kItemSlots];
@@ -448,10 +449,10 @@ __device__ __forceinline__ void load_rows(T (*dst)[64], const T *base, const int
 }
 
 // What the loading warps do, in both directions: take items, and bring their rounds' tiles into the stages
-// through `issue` (which returns the tile's index in its column).
-template <Load LOAD, typename Args, typename Shared, typename Issue>
+// through `issue`; tile_of gives the tile of a round.
+template <Load LOAD, int ROWS, typename Args, typename Shared, typename TileOf, typename Issue>
 __device__ __forceinline__ void load_tiles(const Args &p, Shared &s, const int w, const int lane, const uint32_t rank, const unsigned int C,
-                                           const unsigned int columns, const unsigned int groups, const bool counted, const Issue &issue) {
+                                           const unsigned int columns, const unsigned int groups, const bool counted, const TileOf &tile_of, const Issue &issue) {
     constexpr int kStages = Shared::kStages;
     unsigned int it = 0;
     for (unsigned int q = 0;; ++q) {
@@ -469,6 +470,25 @@ __device__ __forceinline__ void load_tiles(const Args &p, Shared &s, const int w
         const unsigned int seg = done ? 0 : item / columns, col = done ? 0 : item % columns;
         const int r0 = int(seg) * p.pl.iters, r1 = done ? r0 + 1 : int(min(int64_t(r0 + p.pl.iters), p.pl.rounds));
         const unsigned int g = col % groups, b = col / groups;
+        // once an item: the rates; a round ahead: the tile's resets, a lane holding every 32nd step's
+        float rates[2] = {0.25f, 0.25f};
+        unsigned char mark[ROWS / 32] = {};
+        const bool marks = w == 0 && !done && p.reset;
+        const auto look = [&](const int tile) {
+#pragma unroll
+            for (int k = 0; k < ROWS / 32; ++k) {
+                const int64_t t = int64_t(tile) * ROWS + k * 32 + lane;
+                mark[k] = t < p.s.L ? p.reset[int64_t(b) * p.s.L + t] : 0;
+            }
+        };
+        if (w == 0 && !done) {
+            if (marks) look(tile_of(r0));
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const int64_t d = int64_t(g) * 64 + lane * 2 + v;
+                if (d < p.s.D) rates[v] = rate(p.lam[d], p.s.c);
+            }
+        }
         for (int round = r0; round < r1; ++round, ++it) {
             const int st = it % kStages;
             ok = ok && (it < kStages || wait_phase(&s.empty[st], (it / kStages - 1) & 1, &s.abort, p.status));
@@ -479,17 +499,19 @@ __device__ __forceinline__ void load_tiles(const Args &p, Shared &s, const int w
                     asm volatile("cp.async.wait_all;" ::: "memory");
                 return;
             }
-            int tile = -1;
+            const int tile = done ? -1 : tile_of(round);
             if (!done)
-                tile = issue(st, g, b, round);
+                issue(st, g, b, tile);
             else if (LOAD == kTma && lane == 0)
                 mbar_arrive(&s.full[st]);
-            if (w == 0 && !done) {
+            if (w == 0) *reinterpret_cast<float2 *>(&s.rate[st][lane * 2]) = make_float2(rates[0], rates[1]);
+            if (marks) {  // the tile's resets, 32 steps to a word
 #pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const int64_t d = int64_t(g) * 64 + lane * 2 + v;
-                    s.rate[st][lane * 2 + v] = d < p.s.D ? rate(p.lam[d], p.s.c) : 0.25f;
+                for (int k = 0; k < ROWS / 32; ++k) {
+                    const unsigned int word = __ballot_sync(0xffffffffu, mark[k] != 0);
+                    if (lane == 0) s.fresh[st][k] = word;
                 }
+                if (round + 1 < r1) look(tile_of(round + 1));
             }
             if (w == 0 && lane == 0) s.tile[it % kInfos] = {col, seg, tile, (round == r0 ? 1 : 0) | (round == r1 - 1 ? 2 : 0)};
             __syncwarp();
@@ -522,6 +544,7 @@ template <typename T, int K, Load LOAD, bool LAG>
 __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, LAG ? 1 : 2)
     gated_fwd_kernel(const FwdArgs<T> p, const __grid_constant__ Maps3 tm, const bool pairs) {
     static_assert(kChunk % K == 0, "a chunk starts at a warp's first step");
+    static_assert(32 % K == 0 && kW * K % 32 == 0, "a warp's resets lie in one word");
     constexpr int NL = kLoaders<LOAD>, ROWS = kW * K, kStages = FwdShared<T, K, LAG>::kStages;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     FwdShared<T, K, LAG> &s = *reinterpret_cast<FwdShared<T, K, LAG> *>(smem_raw);
@@ -542,8 +565,8 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, LAG ? 1 : 2)
 
     if (warp > kW) {
         // ------------------------------------------------------------ loading
-        load_tiles<LOAD>(p, s, warp - kW - 1, lane, rank, C, columns, groups, counted, [&](const int st, const unsigned int g, const unsigned int b, const int round) {
-            const int tile = round * int(C) + int(rank);
+        load_tiles<LOAD, ROWS>(p, s, warp - kW - 1, lane, rank, C, columns, groups, counted, [&](const int round) { return round * int(C) + int(rank); },
+                         [&](const int st, const unsigned int g, const unsigned int b, const int tile) {
             const int64_t t0 = int64_t(tile) * ROWS;
             if constexpr (LOAD == kTma) {
                 if (lane == 0) {
@@ -559,7 +582,6 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, LAG ? 1 : 2)
                 load_rows<T, ROWS, LOAD, NL>(s.stage[st][1], p.r, b * p.rb + t0 * p.rt + d, p.rt, steps, width, pairs, w, lane);
                 load_rows<T, ROWS, LOAD, NL>(s.stage[st][2], p.i, b * p.ib + t0 * p.it + d, p.it, steps, width, pairs, w, lane);
             }
-            return tile;
         });
     } else if (warp == kW) {
         // ---------------------------------------------------------- the carry
@@ -640,11 +662,7 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, LAG ? 1 : 2)
             if (!__all_sync(0xffffffffu, ok)) return false;
             const TileInfo t = s.tile[it % kInfos];
             if (t.tile < 0) return false;
-            fresh = 0;
-            if (p.reset) {
-                const int64_t tl = int64_t(t.tile) * ROWS + warp * K + lane;
-                fresh = __ballot_sync(0xffffffffu, lane < K && tl < p.s.L && p.reset[int64_t(t.col / groups) * p.s.L + tl] != 0);
-            }
+            fresh = p.reset ? s.fresh[st][warp * K / 32] >> (warp * K % 32) & ((1u << K) - 1u) : 0u;
             const float2 rt = *reinterpret_cast<const float2 *>(&s.rate[st][lane * 2]);
             const T *x = &s.stage[st][0][warp * K][lane * 2], *r = &s.stage[st][1][warp * K][lane * 2],
                     *i = &s.stage[st][2][warp * K][lane * 2];
@@ -762,6 +780,7 @@ struct BwdShared {
     float2 adj[2][kW][32];            // H of its map of the adjoint (P is the same)
     float4 inbox[2][kMaxCluster][32];
     float rate[kStages][64];
+    unsigned int fresh[kStages][(kW * K + 31) / 32];
     TileInfo tile[kInfos];
     uint64_t full[kStages], empty[kStages], posted[2], mail[2], ready[2], told[kItemSlots];
     unsigned int item[kItemSlots];
@@ -882,8 +901,8 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 3
 
     if (warp > kW) {
         // ------------------------------------------------------------ loading
-        load_tiles<LOAD>(p, s, warp - kW - 1, lane, rank, C, columns, groups, counted, [&](const int st, const unsigned int g, const unsigned int b, const int round) {
-            const int tile = int(p.pl.rounds * C) - 1 - (round * int(C) + int(rank));
+        load_tiles<LOAD, ROWS>(p, s, warp - kW - 1, lane, rank, C, columns, groups, counted, [&](const int round) { return int(p.pl.rounds * C) - 1 - (round * int(C) + int(rank)); },
+                         [&](const int st, const unsigned int g, const unsigned int b, const int tile) {
             const int64_t t0 = int64_t(tile) * ROWS;
             if constexpr (LOAD == kTma) {
                 if (lane == 0) {
@@ -901,7 +920,6 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 3
                 load_rows<T, ROWS, LOAD, NL>(s.stage[st][2], p.i, b * p.ib + t0 * p.it + d, p.it, steps, width, pairs, w, lane);
                 load_rows<T, ROWS, LOAD, NL>(s.stage[st][3], p.dy, (int64_t(b) * p.s.L + t0) * p.s.D + d, p.s.D, steps, width, pairs, w, lane);
             }
-            return tile;
         });
     } else if (warp == kW) {
         // ---------------------------------------------------------- the carry
@@ -1006,8 +1024,7 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 3
             const int64_t d = int64_t(t.col % groups) * 64 + lane * 2;
             const int64_t t0 = int64_t(t.tile) * ROWS + warp * K;
             const int steps = int(max(int64_t(0), min(int64_t(K), p.s.L - t0)));
-            unsigned int fresh = 0;
-            if (p.reset) fresh = __ballot_sync(0xffffffffu, lane < steps && p.reset[int64_t(b) * p.s.L + t0 + lane] != 0);
+            const unsigned int fresh = p.reset ? s.fresh[st][warp * K / 32] >> (warp * K % 32) & ((1u << K) - 1u) : 0u;
             const float2 rt = *reinterpret_cast<const float2 *>(&s.rate[st][lane * 2]);
             T *x = &s.stage[st][0][warp * K][lane * 2], *r = &s.stage[st][1][warp * K][lane * 2], *i = &s.stage[st][2][warp * K][lane * 2];
             const T *dy = &s.stage[st][3][warp * K][lane * 2];
