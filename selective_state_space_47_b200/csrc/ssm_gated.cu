@@ -12,11 +12,11 @@
 // passed over once, the state between rounds never leaves the chip, and the order in which pieces are
 // joined depends on the shape alone.
 //
-// What bounds it (B=1 L=65536 D=5120 bfloat16): the forward takes 0.61 ms, 4.4 TB/s of 6.5, with the issue slots at 50%
-// and the special-function unit (four operations an element, 16 a clock) at 52%; the
-// same kernel with the sigmoids left out takes 0.48 ms. The backward takes 1.27 ms, 3.7 TB/s, at 68 instructions and five
-// special-function operations an element. float32, with twice the bytes to the same arithmetic, moves 6.3 TB/s forward and
-// 5.2 TB/s backward (B=8 L=4096 D=2048).
+// What bounds it: the forward of B=1 L=262144 D=5120 bfloat16 takes 2.38 ms, 4.5 TB/s of 6.5, with the issue
+// slots at 53% and the special-function unit (four operations an element, 16 a clock) at 57%; with the
+// sigmoids and the root left out it takes 1.9 ms. The backward of B=8 L=4096 D=2048 takes 262 us, 3.6 TB/s, at 68
+// instructions an element on 51% of the issue slots. float32, with twice the bytes to the same arithmetic,
+// moves 6.3 TB/s forward and 5.2 TB/s backward there.
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <float.h>
