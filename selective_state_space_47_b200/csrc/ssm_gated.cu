@@ -270,10 +270,13 @@ struct FwdArgs {
     float *h_last, *states;
 };
 
-struct TileInfo {
-    unsigned int col, seg;
-    int tile;   // of the column; -1: no more
-    int flags;  // 1: first of its item, 2: last of its item
+struct alignas(16) TileInfo {
+    unsigned int b, g;  // sequence, group of channels
+    int tile;           // of the column; -1: no more
+    unsigned int more;  // steps of the sequence in the tile, flags, segment
+    static constexpr unsigned int kFirst = 1u << 8, kLast = 1u << 9;  // of its item
+    __device__ __forceinline__ int rows() const { return int(more & 255u); }
+    __device__ __forceinline__ unsigned int seg() const { return more >> 10; }
 };
 
 template <typename T, int K, bool LAG>
@@ -403,48 +406,63 @@ __device__ __forceinline__ void copy_async_arrive(uint64_t *bar) {
 template <Load LOAD, bool BWD = false, int SIZE = 0>
 constexpr int kLoaders = LOAD == kTma || (LOAD == kAsync && BWD && SIZE == 2) ? 1 : 3;
 
-// Rows w, w + NL, ... of a tile of one tensor, by one of the loading warps; zeros past the
-// last step and the last channel, as TMA fills them. PAIRS: a lane's two channels lie on
-// their own size; else channels lane and lane + 32 come one by one.
-template <typename T, int ROWS, Load LOAD, int NL>
-__device__ __forceinline__ void load_rows(T (*dst)[64], const T *base, const int64_t at, const int64_t stride, const int steps, const int64_t width,
-                                          const bool pairs, const int w, const int lane) {
-    const T *src = base + at;
-    if constexpr (LOAD == kAsync) {
-        if (pairs) {
-            const bool on = lane * 2 < width;
-            const T *q = src + w * stride + lane * 2;
+// A tensor's tokens, from the first step and channel of a tile on.
+template <typename T>
+struct Source {
+    const T *base;
+    int64_t at, stride;
+};
+
+// Rows w, w + NL, ... of a tile of one tensor, by one of the loading warps, as asynchronous copies; zeros
+// past the last step and the last channel, as TMA fills them. pairs: a lane's two channels
+// lie on their own size; else channels lane and lane + 32 come one by one (float32).
+template <typename T, int ROWS, int NL>
+__device__ __forceinline__ void copy_rows(T (*dst)[64], const Source<T> src, const int steps, const int64_t width, const bool pairs, const int w,
+                                          const int lane) {
+    if (pairs) {
+        const bool on = lane * 2 < width;
+        const T *q = src.base + src.at + w * src.stride + lane * 2;
 #pragma unroll 4
-            for (int k = w; k < ROWS; k += NL, q += NL * stride) copy_async<2 * sizeof(T)>(&dst[k][lane * 2], on && k < steps ? q : base, on && k < steps);
-        } else if constexpr (sizeof(T) == 4) {
-            const bool on0 = lane < width, on1 = lane + 32 < width;
-            const T *q = src + w * stride + lane;
-#pragma unroll 4
-            for (int k = w; k < ROWS; k += NL, q += NL * stride) {
-                copy_async<4>(&dst[k][lane], on0 && k < steps ? q : base, on0 && k < steps);
-                copy_async<4>(&dst[k][lane + 32], on1 && k < steps ? q + 32 : base, on1 && k < steps);
-            }
-        }
-    } else {
-        constexpr int N = 8;
+        for (int k = w; k < ROWS; k += NL, q += NL * src.stride)
+            copy_async<2 * sizeof(T)>(&dst[k][lane * 2], on && k < steps ? q : src.base, on && k < steps);
+    } else if constexpr (sizeof(T) == 4) {
         const bool on0 = lane < width, on1 = lane + 32 < width;
-        const T *q = src + w * stride + lane;
-        for (int k0 = w; k0 < ROWS; k0 += NL * N, q += NL * N * stride) {
-            T v[N][2];
+        const T *q = src.base + src.at + w * src.stride + lane;
+#pragma unroll 4
+        for (int k = w; k < ROWS; k += NL, q += NL * src.stride) {
+            copy_async<4>(&dst[k][lane], on0 && k < steps ? q : src.base, on0 && k < steps);
+            copy_async<4>(&dst[k][lane + 32], on1 && k < steps ? q + 32 : src.base, on1 && k < steps);
+        }
+    }
+}
+
+// The same element by element, through registers: N rows of all the tensors at a time, since what is on its way
+// at once sets the rate (three tensors one after the other: 148 us for B=2 L=8191 D=1001 forward).
+template <typename T, int ROWS, int NL, int NT>
+__device__ __forceinline__ void move_rows(T (*dst)[ROWS][64], const Source<T> (&src)[NT], const int steps, const int64_t width, const int w,
+                                          const int lane) {
+    constexpr int N = 8;
+    const bool on0 = lane < width, on1 = lane + 32 < width;
+    for (int k0 = w; k0 < ROWS; k0 += NL * N) {
+        T v[NT][N][2];
 #pragma unroll
-            for (int n = 0; n < N; ++n) {
+        for (int t = 0; t < NT; ++t) {
+            const T *q = src[t].base + src[t].at + k0 * src[t].stride + lane;
+#pragma unroll
+            for (int n = 0; n < N; ++n, q += NL * src[t].stride) {
                 const bool in = k0 + NL * n < min(ROWS, steps);
-                v[n][0] = on0 && in ? q[NL * n * stride] : Tok<T>::from_f(0.0f);
-                v[n][1] = on1 && in ? q[NL * n * stride + 32] : Tok<T>::from_f(0.0f);
-            }
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                if (k0 + NL * n < ROWS) {
-                    dst[k0 + NL * n][lane] = v[n][0];
-                    dst[k0 + NL * n][lane + 32] = v[n][1];
-                }
+                v[t][n][0] = on0 && in ? q[0] : Tok<T>::from_f(0.0f);
+                v[t][n][1] = on1 && in ? q[32] : Tok<T>::from_f(0.0f);
             }
         }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                if (k0 + NL * n < ROWS) {
+                    dst[t][k0 + NL * n][lane] = v[t][n][0];
+                    dst[t][k0 + NL * n][lane + 32] = v[t][n][1];
+                }
     }
 }
 
@@ -513,7 +531,10 @@ __device__ __forceinline__ void load_tiles(const Args &p, Shared &s, const int w
                 }
                 if (round + 1 < r1) look(tile_of(round + 1));
             }
-            if (w == 0 && lane == 0) s.tile[it % kInfos] = {col, seg, tile, (round == r0 ? 1 : 0) | (round == r1 - 1 ? 2 : 0)};
+            if (w == 0 && lane == 0) {
+                const unsigned int rows = unsigned(max(int64_t(0), min(int64_t(ROWS), p.s.L - int64_t(tile) * ROWS)));
+                s.tile[it % kInfos] = {b, g, tile, rows | (round == r0 ? TileInfo::kFirst : 0u) | (round == r1 - 1 ? TileInfo::kLast : 0u) | seg << 10};
+            }
             __syncwarp();
             if (w == 0 && lane == 0) mbar_arrive(&s.full[st]);
             if (LOAD == kAsync)
@@ -545,6 +566,8 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, LAG ? 1 : 2)
     gated_fwd_kernel(const FwdArgs<T> p, const __grid_constant__ Maps3 tm, const bool pairs) {
     static_assert(kChunk % K == 0, "a chunk starts at a warp's first step");
     static_assert(32 % K == 0 && kW * K % 32 == 0, "a warp's resets lie in one word");
+    static_assert(kW * K < 256, "a tile's steps take eight bits");
+    static_assert(LAG || sizeof(FwdShared<T, K, LAG>) <= 228 * 1024 / 2 - 1024, "two blocks share an SM");
     constexpr int NL = kLoaders<LOAD>, ROWS = kW * K, kStages = FwdShared<T, K, LAG>::kStages;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     FwdShared<T, K, LAG> &s = *reinterpret_cast<FwdShared<T, K, LAG> *>(smem_raw);
@@ -578,9 +601,13 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, LAG ? 1 : 2)
             } else {
                 const int w = warp - kW - 1, steps = int(max(int64_t(0), min(int64_t(ROWS), p.s.L - t0)));
                 const int64_t d = int64_t(g) * 64, width = p.s.D - d;
-                load_rows<T, ROWS, LOAD, NL>(s.stage[st][0], p.x, b * p.xb + t0 * p.xt + d, p.xt, steps, width, pairs, w, lane);
-                load_rows<T, ROWS, LOAD, NL>(s.stage[st][1], p.r, b * p.rb + t0 * p.rt + d, p.rt, steps, width, pairs, w, lane);
-                load_rows<T, ROWS, LOAD, NL>(s.stage[st][2], p.i, b * p.ib + t0 * p.it + d, p.it, steps, width, pairs, w, lane);
+                const Source<T> src[3] = {{p.x, b * p.xb + t0 * p.xt + d, p.xt}, {p.r, b * p.rb + t0 * p.rt + d, p.rt}, {p.i, b * p.ib + t0 * p.it + d, p.it}};
+                if constexpr (LOAD == kPlain) {
+                    move_rows<T, ROWS, NL>(s.stage[st], src, steps, width, w, lane);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 3; ++t) copy_rows<T, ROWS, NL>(s.stage[st][t], src[t], steps, width, pairs, w, lane);
+                }
             }
         });
     } else if (warp == kW) {
@@ -595,7 +622,7 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, LAG ? 1 : 2)
             __syncwarp();
             // (a stage is refilled once this warp has seen it too: a phase it misses would look like one to come)
             if (lane == 0) mbar_arrive(&s.empty[it % kStages]);
-            const int64_t d = int64_t(t.col % groups) * 64 + lane * 2, o = int64_t(t.col / groups) * p.s.D + d;
+            const int64_t d = int64_t(t.g) * 64 + lane * 2, o = int64_t(t.b) * p.s.D + d;
             const int have = int(min(int64_t(2), p.s.D - d));  // channels of this lane (at most 2)
             const int buf = it & 1;
             const uint32_t phase = (it >> 1) & 1;
@@ -609,12 +636,12 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, LAG ? 1 : 2)
             if (C > 1)
                 for (unsigned int k = 0; k < C; ++k)
                     send16(peer_addr(&s.inbox[buf][rank][lane], k), own, peer_addr(&s.mail[buf], k));
-            if (t.flags & 1) {
+            if (t.more & TileInfo::kFirst) {
                 S = two(0.0f);
                 M = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
                 if (!p.maps) {
-                    const unsigned long long *q = p.starts + int64_t(t.seg) * n + o;
-                    if (t.seg == 0) {
+                    const unsigned long long *q = p.starts + int64_t(t.seg()) * n + o;
+                    if (t.seg() == 0) {
                         if (p.h0 && have > 0) S.x = p.h0[o];
                         if (p.h0 && have > 1) S.y = p.h0[o + 1];
                     } else {
@@ -642,12 +669,12 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, LAG ? 1 : 2)
             for (int w = 0; w < kW; ++w) *reinterpret_cast<float2 *>(&s.maps[buf][w][lane]) = e[w];
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.ready[buf]);
-            if ((t.flags & 2) && rank == 0) {
+            if ((t.more & TileInfo::kLast) && rank == 0) {
                 if (p.maps) {
-                    if (have > 0) p.maps[int64_t(t.seg) * n + o] = Map{M.x, M.y};
-                    if (have > 1) p.maps[int64_t(t.seg) * n + o + 1] = Map{M.z, M.w};
-                } else if (counted && int(t.seg) + 1 < p.pl.segs) {
-                    unsigned long long *q = p.starts + int64_t(t.seg + 1) * n + o;
+                    if (have > 0) p.maps[int64_t(t.seg()) * n + o] = Map{M.x, M.y};
+                    if (have > 1) p.maps[int64_t(t.seg()) * n + o + 1] = Map{M.z, M.w};
+                } else if (counted && int(t.seg()) + 1 < p.pl.segs) {
+                    unsigned long long *q = p.starts + int64_t(t.seg() + 1) * n + o;
                     if (have > 0) st_word(q, pack(S.x));
                     if (have > 1) st_word(q + 1, pack(S.y));
                 }
@@ -682,10 +709,10 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, LAG ? 1 : 2)
         const auto write = [&](const unsigned int it, const float2(&a)[K], const float2(&h)[K], const unsigned int fresh) {
             wait_phase(&s.ready[it & 1], (it >> 1) & 1, &s.abort, p.status);
             const TileInfo t = s.tile[it % kInfos];
-            const unsigned int b = t.col / groups;
-            const int64_t d = int64_t(t.col % groups) * 64 + lane * 2;
+            const unsigned int b = t.b;
+            const int64_t d = int64_t(t.g) * 64 + lane * 2;
             const int64_t t0 = int64_t(t.tile) * ROWS + warp * K;
-            const int steps = int(max(int64_t(0), min(int64_t(K), p.s.L - t0)));
+            const int steps = max(0, min(K, t.rows() - warp * K));
             if (!p.maps && d < p.s.D && steps > 0) {
                 float2 hs = *reinterpret_cast<const float2 *>(&s.maps[it & 1][warp][lane]);
                 const bool both = d + 1 < p.s.D;
@@ -915,10 +942,14 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 3
             } else {
                 const int w = warp - kW - 1, steps = int(max(int64_t(0), min(int64_t(ROWS), p.s.L - t0)));
                 const int64_t d = int64_t(g) * 64, width = p.s.D - d;
-                load_rows<T, ROWS, LOAD, NL>(s.stage[st][0], p.x, b * p.xb + t0 * p.xt + d, p.xt, steps, width, pairs, w, lane);
-                load_rows<T, ROWS, LOAD, NL>(s.stage[st][1], p.r, b * p.rb + t0 * p.rt + d, p.rt, steps, width, pairs, w, lane);
-                load_rows<T, ROWS, LOAD, NL>(s.stage[st][2], p.i, b * p.ib + t0 * p.it + d, p.it, steps, width, pairs, w, lane);
-                load_rows<T, ROWS, LOAD, NL>(s.stage[st][3], p.dy, (int64_t(b) * p.s.L + t0) * p.s.D + d, p.s.D, steps, width, pairs, w, lane);
+                const Source<T> src[4] = {{p.x, b * p.xb + t0 * p.xt + d, p.xt}, {p.r, b * p.rb + t0 * p.rt + d, p.rt}, {p.i, b * p.ib + t0 * p.it + d, p.it},
+                                          {p.dy, (int64_t(b) * p.s.L + t0) * p.s.D + d, p.s.D}};
+                if constexpr (LOAD == kPlain) {
+                    move_rows<T, ROWS, NL>(s.stage[st], src, steps, width, w, lane);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) copy_rows<T, ROWS, NL>(s.stage[st][t], src[t], steps, width, pairs, w, lane);
+                }
             }
         });
     } else if (warp == kW) {
@@ -932,8 +963,8 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 3
             if (t.tile < 0) break;
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.empty[it % kStages]);
-            const unsigned int b = t.col / groups;
-            const int64_t d = int64_t(t.col % groups) * 64 + lane * 2, o = int64_t(b) * p.s.D + d;
+            const unsigned int b = t.b;
+            const int64_t d = int64_t(t.g) * 64 + lane * 2, o = int64_t(b) * p.s.D + d;
             const int have = int(min(int64_t(2), p.s.D - d));  // channels of this lane (at most 2)
             const int buf = it & 1;
             const uint32_t phase = (it >> 1) & 1;
@@ -957,12 +988,12 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 3
             if (C > 1)
                 for (unsigned int k = 0; k < C; ++k)
                     send16(peer_addr(&s.inbox[buf][rank][lane], k), own, peer_addr(&s.mail[buf], k));
-            if (t.flags & 1) {
+            if (t.more & TileInfo::kFirst) {
                 S = two(0.0f);
                 M = make_float4(1.0f, 0.0f, 1.0f, 0.0f);
                 if (!p.maps) {
-                    const unsigned long long *q = p.starts + int64_t(t.seg) * n + o;
-                    if (t.seg == 0) {
+                    const unsigned long long *q = p.starts + int64_t(t.seg()) * n + o;
+                    if (t.seg() == 0) {
                         if (p.dh_last && have > 0) S.x = p.dh_last[o];
                         if (p.dh_last && have > 1) S.y = p.dh_last[o + 1];
                     } else {
@@ -997,15 +1028,15 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 3
             for (int w = 0; w < kW; ++w) reinterpret_cast<float2 *>(&s.maps[buf][w][lane])[1] = e[kW - 1 - w];
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.ready[buf]);
-            if ((t.flags & 2) && rank == 0) {
+            if ((t.more & TileInfo::kLast) && rank == 0) {
                 if (p.maps) {
-                    if (have > 0) p.maps[int64_t(t.seg) * n + o] = Map{M.x, M.y};
-                    if (have > 1) p.maps[int64_t(t.seg) * n + o + 1] = Map{M.z, M.w};
-                } else if (int(t.seg) + 1 == p.pl.segs) {
+                    if (have > 0) p.maps[int64_t(t.seg()) * n + o] = Map{M.x, M.y};
+                    if (have > 1) p.maps[int64_t(t.seg()) * n + o + 1] = Map{M.z, M.w};
+                } else if (int(t.seg()) + 1 == p.pl.segs) {
                     if (p.dh0 && have > 0) p.dh0[o] = S.x;
                     if (p.dh0 && have > 1) p.dh0[o + 1] = S.y;
                 } else if (counted) {
-                    unsigned long long *q = p.starts + int64_t(t.seg + 1) * n + o;
+                    unsigned long long *q = p.starts + int64_t(t.seg() + 1) * n + o;
                     if (have > 0) st_word(q, pack(S.x));
                     if (have > 1) st_word(q + 1, pack(S.y));
                 }
@@ -1020,10 +1051,10 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 3
             if (!__all_sync(0xffffffffu, ok)) break;
             const TileInfo t = s.tile[it % kInfos];
             if (t.tile < 0) break;
-            const unsigned int b = t.col / groups;
-            const int64_t d = int64_t(t.col % groups) * 64 + lane * 2;
+            const unsigned int b = t.b;
+            const int64_t d = int64_t(t.g) * 64 + lane * 2;
             const int64_t t0 = int64_t(t.tile) * ROWS + warp * K;
-            const int steps = int(max(int64_t(0), min(int64_t(K), p.s.L - t0)));
+            const int steps = max(0, min(K, t.rows() - warp * K));
             const unsigned int fresh = p.reset ? s.fresh[st][warp * K / 32] >> (warp * K % 32) & ((1u << K) - 1u) : 0u;
             const float2 rt = *reinterpret_cast<const float2 *>(&s.rate[st][lane * 2]);
             T *x = &s.stage[st][0][warp * K][lane * 2], *r = &s.stage[st][1][warp * K][lane * 2], *i = &s.stage[st][2][warp * K][lane * 2];
@@ -1047,7 +1078,7 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 3
             if (!p.maps) {
                 const float4 begin = s.maps[buf][warp][lane];
                 const float2 hs = make_float2(begin.x, begin.y), gs = make_float2(begin.z, begin.w);
-                if (t.flags & 1) dl = two(0.0f);
+                if (t.more & TileInfo::kFirst) dl = two(0.0f);
                 if constexpr (LOAD == kTma) {
                     const auto out = [&](const int k, const float2 gx, const float2 gr, const float2 gi) {
                         store2(x + k * 64, gx);
@@ -1079,8 +1110,8 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 3
                     dl = add2(dl, slow ? bwd_grads_of<T, K, false>(x, dy, rt, fresh, steps, a, h, sr, si, hs, gs, out)
                                        : bwd_grads_of<T, K, true>(x, dy, rt, fresh, steps, a, h, sr, si, hs, gs, out));
                 }
-                if (t.flags & 2) {
-                    float *q = p.parts + (((int64_t(t.seg) * C + rank) * kW + warp) * p.s.B + b) * p.s.D + d;
+                if (t.more & TileInfo::kLast) {
+                    float *q = p.parts + (((int64_t(t.seg()) * C + rank) * kW + warp) * p.s.B + b) * p.s.D + d;
                     if (d < p.s.D) q[0] = dl.x;
                     if (d + 1 < p.s.D) q[1] = dl.y;
                 }
