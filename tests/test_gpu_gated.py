@@ -318,6 +318,21 @@ def test_step_chain(ssm, size, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,D", [(700, 1024), (4099, 258), (70001, 4)])
+def test_step_of_large_batches(ssm, B, D, dtype):
+    """Many sequences to a thread, batches that are no multiple of them, arrays that start off a whole piece, and
+    a large rate."""
+    d = make(B, 1, D, dtype, seed=B, h0=True, slow=False)
+    g = cuda(d)
+    want, bound = ref.gated_scan(*(d[k] for k in FWD))
+    buf = torch.empty(B * D + 1, device="cuda")
+    for h in (g["h0"].clone(), buf[1:].view(B, D).copy_(g["h0"])):
+        y = ssm.gated_step(*(g[k][:, 0] for k in ("x", "r", "i")), g["lam"], h)
+        ref.check(y, want[:, 0], bound[:, 0], dtype, "y")
+        ref.check(h, want[:, 0], bound[:, 0], what="h")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 def test_autograd(ssm, dtype):
     d = make(2, 260, 36, dtype, seed=31, h0=True, reset=0.01)
     g = cuda(d)
