@@ -396,14 +396,15 @@ ssm_status ssm_ssd_fwd(const ssm_ssd_args *args, void *stream);
  * and, where reset[b, t] is not 0 (a new document begins), a_t = 0 and beta_t = 1: the
  * state before it is dropped, whatever it holds. The state and every factor are float32
  * (1 - a_t is formed without cancellation); y is rounded once. Neighbouring pieces of
- * time are combined in an order that depends on the shape alone, so results repeat bit
- * for bit.
+ * time are combined in an order that depends on the shape, the strides and the GPU alone,
+ * so results repeat bit for bit. ssm_workspace_status() reports a bounded device-side wait that
+ * gave up (SSM_ERR_TIMEOUT: that call's outputs are not valid), here and in the backward.
  *
  * x, r, i may be strided: element [b, t, d] of x lies at x + b x_stride[0] + t x_stride[1]
- * + d (strides in elements, not negative), so that slices of one projection are read in
- * place. All other arrays are contiguous. Any dim and seqlen; tokens on their element
- * size, float arrays on 4 bytes. Where dim and the strides are even and the token arrays
- * start on two elements (float arrays on 8 bytes), a lane takes two channels.
+ * + d (strides in elements, not negative; one over a single sequence or step does not count), so
+ * that slices of one projection are read in place. All other arrays are contiguous. Any dim
+ * and seqlen; tokens on their element size, float arrays on 4 bytes. Token rows on 16 bytes are
+ * fetched by TMA, others in pieces of two elements or element by element (slower).
  *
  * states (optional output) receives what the backward needs of the forward: the state
  * before every SSM_GATED_CHUNK-th step, [B, ceil(L / SSM_GATED_CHUNK), D] float32

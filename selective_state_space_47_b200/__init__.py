@@ -674,6 +674,12 @@ def _as_grad(g, like, dtype):
     return g if g.dtype is dtype and g.is_contiguous() else g.to(dtype).contiguous()
 
 
+def _once(backward):
+    """once_differentiable, whose own bookkeeping is skipped where no graph of the backward is kept."""
+    kept = torch.autograd.function.once_differentiable(backward)
+    return lambda ctx, *grads: kept(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
+
+
 class _GatedScan(torch.autograd.Function):
     """gated_scan_fwd as an autograd function; of the forward it keeps the inputs and the
     states before every chunk."""
@@ -687,7 +693,7 @@ class _GatedScan(torch.autograd.Function):
         return res[:-1] if last else res[0]
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_once
     def backward(ctx, dy, dh_last=None):
         x, r, i, lam, reset, states = ctx.saved_tensors
         if dy is None and dh_last is None:
@@ -805,7 +811,7 @@ class _LayerNorm(torch.autograd.Function):
         return res[0] if residual is None else res[:2]
 
     @staticmethod
-    @torch.autograd.function.once_differentiable
+    @_once
     def backward(ctx, dy, ds=None):
         s, weight, mean, rstd = ctx.saved_tensors
         if dy is None and ds is None:

@@ -12,9 +12,9 @@
 // passed over once, the state between rounds never leaves the chip, and the order in which pieces are
 // joined depends on the shape alone.
 //
-// What bounds it: the forward of B=1 L=262144 D=5120 bfloat16 takes 2.38 ms, 4.5 TB/s of 6.5, with the issue
+// What bounds it: the forward of B=1 L=262144 D=5120 bfloat16 takes 2.29 ms, 4.7 TB/s of 6.5, with the issue
 // slots at 53% and the special-function unit (four operations an element, 16 a clock) at 57%; with the
-// sigmoids and the root left out it takes 1.9 ms. The backward of B=8 L=4096 D=2048 takes 262 us, 3.6 TB/s, at 68
+// sigmoids and the root left out it takes 1.9 ms. The backward of B=8 L=4096 D=2048 takes 255 us, 3.7 TB/s, at 68
 // instructions an element on 51% of the issue slots. float32, with twice the bytes to the same arithmetic,
 // moves 6.3 TB/s forward and 5.2 TB/s backward there.
 #include <cudaTypedefs.h>

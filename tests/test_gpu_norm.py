@@ -158,6 +158,17 @@ def test_autograd(ssm, dtype):
     assert torch.equal(gr, g["dres"]) and torch.equal(gw, torch.zeros_like(gw))
 
 
+def test_a_second_derivative_is_refused(ssm):
+    x = torch.randn(4, 32, device="cuda", requires_grad=True)
+    w = torch.ones(32, device="cuda")
+    for y in (ssm.layer_norm(x, w), ssm.gated_scan(x[None], x[None], x[None], w)):
+        g, = torch.autograd.grad(y.square().sum(), x, create_graph=True)  # the first one is as without a graph
+        y2 = ssm.layer_norm(x, w) if y.dim() == 2 else ssm.gated_scan(x[None], x[None], x[None], w)
+        assert torch.equal(g, torch.autograd.grad(y2.square().sum(), x)[0])
+        with pytest.raises(RuntimeError):
+            torch.autograd.grad(g.sum(), x)
+
+
 def test_graph(ssm):
     d = make(64, 256, BF16, 17, True)
     g = cuda(d)
