@@ -422,7 +422,15 @@ struct Source {
 template <typename T, int ROWS, int NL>
 __device__ __forceinline__ void copy_rows(T (*dst)[64], const Source<T> src, const int steps, const int64_t width, const bool pairs, const int w,
                                           const int lane) {
-    if (pairs) {
+    if (pairs && steps >= ROWS && width >= 64) {  // a whole tile: nothing to ask
+        const T *q = src.base + src.at + w * src.stride + lane * 2;
+        const uint32_t to = smem_u32(&dst[w][lane * 2]);
+#pragma unroll 8
+        for (int k = 0; k < ROWS / NL; ++k, q += NL * src.stride)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to + k * NL * 64 * int(sizeof(T))), "l"(q), "n"(2 * sizeof(T)) : "memory");
+        if (w < ROWS % NL)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to + ROWS / NL * NL * 64 * int(sizeof(T))), "l"(q), "n"(2 * sizeof(T)) : "memory");
+    } else if (pairs) {
         const bool on = lane * 2 < width;
         const T *q = src.base + src.at + w * src.stride + lane * 2;
 #pragma unroll 4
