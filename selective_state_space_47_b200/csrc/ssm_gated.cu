@@ -305,11 +305,11 @@ constexpr int kFewColumns = 24;  // up to here LAG: 1536 channels of one sequenc
 
 enum Load { kTma, kAsync, kPlain };  // 16-byte rows; pieces of 4 or 8 bytes; elements of 2 bytes
 
-// Decays and inputs of a thread's steps, and their map. FAST: no reset among them, every rate
+// Decays and inputs of a thread's steps, and their map. RESETS: there may be some among them. FAST: every rate
 // between 1e-18 and 1/2 (neither the decay's exponential nor a case for beta = 0 is
 // needed), and one reciprocal serves both sigmoids: 1/(1+E) = (1+F)/((1+E)(1+F)); `big`
 // tells of gates below -41, whose exponentials' product could overflow and w underflow.
-template <typename T, int K, bool FAST>
+template <typename T, int K, bool FAST, bool RESETS>
 __device__ __forceinline__ float4 fwd_steps_of(const T *x, const T *r, const T *i, const float2 rt, const unsigned int fresh,
                                                float2 (&a)[K], float2 (&h)[K], float &big) {
     float2 P = two(1.0f), H = two(0.0f);
@@ -336,7 +336,7 @@ __device__ __forceinline__ float4 fwd_steps_of(const T *x, const T *r, const T *
             h[k] = mul2(mul2(sq, make_float2(rsqrt_approx(sq.x), rsqrt_approx(sq.y))), u);
         else
             h[k] = mul2(make_float2(sqrt_approx(sq.x), sqrt_approx(sq.y)), u);
-        const bool fr = !FAST && (fresh >> k & 1);
+        const bool fr = RESETS && (fresh >> k & 1);
         if (fr) h[k] = u;
         P = mul2(P, a[k]);
         H = fr ? h[k] : fma2(a[k], H, h[k]);
@@ -479,7 +479,7 @@ __device__ __forceinline__ void move_rows(T (*dst)[ROWS][64], const Source<T> (&
 
 // What the loading warps do, in both directions: take items, and bring their rounds' tiles into the stages
 // through `issue`; tile_of gives the tile of a round.
-template <Load LOAD, int ROWS, typename Args, typename Shared, typename TileOf, typename Issue>
+template <Load LOAD, bool RESETS, int ROWS, typename Args, typename Shared, typename TileOf, typename Issue>
 __device__ __forceinline__ void load_tiles(const Args &p, Shared &s, const int w, const int lane, const uint32_t rank, const unsigned int C,
                                            const unsigned int columns, const unsigned int groups, const bool counted, const TileOf &tile_of, const Issue &issue) {
     constexpr int kStages = Shared::kStages;
@@ -502,7 +502,7 @@ __device__ __forceinline__ void load_tiles(const Args &p, Shared &s, const int w
         // once an item: the rates; a round ahead: the tile's resets, a lane holding every 32nd step's
         float rates[2] = {0.25f, 0.25f};
         unsigned char mark[ROWS / 32] = {};
-        const bool marks = w == 0 && !done && p.reset;
+        const bool marks = RESETS && w == 0 && !done;
         const auto look = [&](const int tile) {
 #pragma unroll
             for (int k = 0; k < ROWS / 32; ++k) {
@@ -572,7 +572,9 @@ __device__ __forceinline__ void load_tiles(const Args &p, Shared &s, const int w
 // start is there, and no warp waits for the way to the cluster and back. That takes the registers of a whole SM per
 // block. It pays where there are too few columns for two blocks an SM anyway (B=1 L=131072 D=1024: 481 -> 340 us, D=512 263 -> 189 us);
 // with enough of them the other block fills the wait (D=2048: 587 us without, 707 with).
-template <typename T, int K, Load LOAD, bool LAG>
+// RESETS: there is a reset array (its selections in a kernel that never uses them cost registers: 583 against 615 us for
+// L=65536 D=5120).
+template <typename T, int K, Load LOAD, bool LAG, bool RESETS>
 __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, LAG ? 1 : 2)
     gated_fwd_kernel(const FwdArgs<T> p, const __grid_constant__ Maps3 tm, const bool pairs) {
     static_assert(kChunk % K == 0, "a chunk starts at a warp's first step");
@@ -599,7 +601,7 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, LAG ? 1 : 2)
 
     if (warp > kW) {
         // ------------------------------------------------------------ loading
-        load_tiles<LOAD, ROWS>(p, s, warp - kW - 1, lane, rank, C, columns, groups, counted, [&](const int round) { return round * int(C) + int(rank); },
+        load_tiles<LOAD, RESETS, ROWS>(p, s, warp - kW - 1, lane, rank, C, columns, groups, counted, [&](const int round) { return round * int(C) + int(rank); },
                          [&](const int st, const unsigned int g, const unsigned int b, const int tile) {
             const int64_t t0 = int64_t(tile) * ROWS;
             if constexpr (LOAD == kTma) {
@@ -700,15 +702,16 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, LAG ? 1 : 2)
             if (!__all_sync(0xffffffffu, ok)) return false;
             const TileInfo t = s.tile[it % kInfos];
             if (t.tile < 0) return false;
-            fresh = p.reset ? s.fresh[st][warp * K / 32] >> (warp * K % 32) & ((1u << K) - 1u) : 0u;
+            fresh = RESETS ? s.fresh[st][warp * K / 32] >> (warp * K % 32) & ((1u << K) - 1u) : 0u;
             const float2 rt = *reinterpret_cast<const float2 *>(&s.rate[st][lane * 2]);
             const T *x = &s.stage[st][0][warp * K][lane * 2], *r = &s.stage[st][1][warp * K][lane * 2],
                     *i = &s.stage[st][2][warp * K][lane * 2];
             float4 m;
             float big = 1e30f;
-            if (fresh == 0 && __all_sync(0xffffffffu, fmaxf(rt.x, rt.y) < 0.5f && fminf(rt.x, rt.y) > 1e-18f))
-                m = fwd_steps_of<T, K, true>(x, r, i, rt, fresh, a, h, big);
-            if (__any_sync(0xffffffffu, big > 60.0f)) m = fwd_steps_of<T, K, false>(x, r, i, rt, fresh, a, h, big);
+            if (__all_sync(0xffffffffu, fmaxf(rt.x, rt.y) < 0.5f && fminf(rt.x, rt.y) > 1e-18f))
+                m = !RESETS || fresh == 0 ? fwd_steps_of<T, K, true, false>(x, r, i, rt, 0u, a, h, big)
+                                          : fwd_steps_of<T, K, true, RESETS>(x, r, i, rt, fresh, a, h, big);
+            if (__any_sync(0xffffffffu, big > 60.0f)) m = fwd_steps_of<T, K, false, RESETS>(x, r, i, rt, fresh, a, h, big);
             s.maps[it & 1][warp][lane] = m;
             __syncwarp();
             if (lane == 0) {
@@ -733,17 +736,23 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, LAG ? 1 : 2)
                     if (both) q[1] = hs.y;
                 }
                 T *yp = p.y + (int64_t(b) * p.s.L + t0) * p.s.D + d;
-                if (steps == K && fresh == 0 && p.y && pairs) {
+                if (steps == K && (!RESETS || fresh == 0) && p.y && pairs) {
 #pragma unroll
                     for (int k = 0; k < K; ++k, yp += p.s.D) {
                         hs = fma2(a[k], hs, h[k]);
+                        store2(yp, hs);
+                    }
+                } else if (RESETS && steps == K && p.y && pairs) {
+#pragma unroll
+                    for (int k = 0; k < K; ++k, yp += p.s.D) {
+                        hs = (fresh >> k & 1) ? h[k] : fma2(a[k], hs, h[k]);
                         store2(yp, hs);
                     }
                 } else {
 #pragma unroll
                     for (int k = 0; k < K; ++k, yp += p.s.D)
                         if (k < steps) {
-                            hs = (fresh >> k & 1) ? h[k] : fma2(a[k], hs, h[k]);
+                            hs = RESETS && (fresh >> k & 1) ? h[k] : fma2(a[k], hs, h[k]);
                             if (p.y && pairs) {
                                 store2(yp, hs);
                             } else if (p.y) {
@@ -832,7 +841,7 @@ struct Maps7 {
 // v_t = dL/dh_t follows v_t = dy_t + a_{t+1} v_{t+1}; with g_t = a_t v_t, what a step hands to
 // the one before it, a piece of time acts on the g entering from its right as g -> P g + G
 // with the forward's P. Steps past the end are the identity.
-template <typename T, int K, bool FAST>
+template <typename T, int K, bool FAST, bool RESETS>
 __device__ __forceinline__ void bwd_steps_of(const T *x, const T *r, const T *i, const T *dy, const float2 rt, const unsigned int fresh,
                                              const int steps, float2 (&a)[K], float2 (&h)[K], float2 (&sr)[K], float2 (&si)[K],
                                              float4 &f, float2 &g, float &big) {
@@ -856,21 +865,19 @@ __device__ __forceinline__ void bwd_steps_of(const T *x, const T *r, const T *i,
         a[k] = decay2<FAST>(mul2(rt, sr[k]), e);
         const float2 sq = mul2(e, fma2(e, two(-1.0f), two(2.0f)));
         const float2 u = mul2(si[k], load2(x + k * 64));
-        if constexpr (FAST) {
+        if constexpr (FAST)
             h[k] = mul2(mul2(sq, make_float2(rsqrt_approx(sq.x), rsqrt_approx(sq.y))), u);
-            P = mul2(P, a[k]);
-            H = fma2(a[k], H, h[k]);
-        } else {
-            const bool fr = fresh >> k & 1;
-            h[k] = fr ? u : mul2(make_float2(sqrt_approx(sq.x), sqrt_approx(sq.y)), u);
-            if (k >= steps) a[k] = two(1.0f);
-            P = mul2(P, a[k]);
-            H = fr ? h[k] : fma2(a[k], H, h[k]);
-        }
+        else
+            h[k] = mul2(make_float2(sqrt_approx(sq.x), sqrt_approx(sq.y)), u);
+        const bool fr = RESETS && (fresh >> k & 1);
+        if (fr) h[k] = u;
+        if (!FAST && k >= steps) a[k] = two(1.0f);
+        P = mul2(P, a[k]);
+        H = fr ? h[k] : fma2(a[k], H, h[k]);
     }
 #pragma unroll
     for (int k = K - 1; k >= 0; --k) {
-        if (FAST || k < steps) G = (!FAST && (fresh >> k & 1)) ? two(0.0f) : mul2(a[k], add2(load2(dy + k * 64), G));
+        if (FAST || k < steps) G = RESETS && (fresh >> k & 1) ? two(0.0f) : mul2(a[k], add2(load2(dy + k * 64), G));
     }
     big = top;
     f = make_float4(fresh ? 0.0f : keep(P.x), H.x, fresh ? 0.0f : keep(P.y), H.y);
@@ -879,13 +886,13 @@ __device__ __forceinline__ void bwd_steps_of(const T *x, const T *r, const T *i,
 
 // The gradients of a thread's steps, from the state entering them on the left and the adjoint on the right, given
 // to out(k, dx, dr, di) from the last step to the first; the sum of dw sigmoid(r).
-template <typename T, int K, bool FAST, typename Out>
+template <typename T, int K, bool FAST, bool RESETS, typename Out>
 __device__ __forceinline__ float2 bwd_grads_of(const T *x, const T *dy, const float2 rt, const unsigned int fresh, const int steps,
                                                const float2 (&a)[K], float2 (&h)[K], const float2 (&sr)[K], const float2 (&si)[K],
                                                float2 hs, float2 gs, const Out &out) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {  // h[k]: the state before the step
-        const float2 next = (!FAST && (fresh >> k & 1)) ? h[k] : fma2(a[k], hs, h[k]);
+        const float2 next = RESETS && (fresh >> k & 1) ? h[k] : fma2(a[k], hs, h[k]);
         h[k] = hs;
         hs = next;
     }
@@ -893,7 +900,7 @@ __device__ __forceinline__ float2 bwd_grads_of(const T *x, const T *dy, const fl
 #pragma unroll
     for (int k = K - 1; k >= 0; --k) {
         if (!FAST && k >= steps) continue;
-        const bool fr = !FAST && (fresh >> k & 1);
+        const bool fr = RESETS && (fresh >> k & 1);
         const float2 v = add2(load2(dy + k * 64), gs), w = mul2(rt, sr[k]), u = mul2(si[k], load2(x + k * 64));
         float2 e = small_e2(w);
         if (!FAST) e = make_float2(w.x < 0.5f ? e.x : 1.0f - a[k].x, w.y < 0.5f ? e.y : 1.0f - a[k].y);
@@ -915,7 +922,7 @@ __device__ __forceinline__ float2 bwd_grads_of(const T *x, const T *dy, const fl
 // is known, so only the adjoint passes from block to block. The decays, inputs and sigmoids of a thread's
 // steps stay in registers between the two passes over them; a tile's tokens stay in
 // its stage until its gradients, written over them, have left.
-template <typename T, int K, Load LOAD>
+template <typename T, int K, Load LOAD, bool RESETS>
 __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 32, sizeof(T) == 2 ? 2 : 1)
     gated_bwd_kernel(const BwdArgs<T> p, const __grid_constant__ Maps7 tm, const bool pairs) {
     constexpr int NL = kLoaders<LOAD, true, sizeof(T)>, ROWS = kW * K, kStages = BwdShared<T, K>::kStages;
@@ -939,7 +946,7 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 3
 
     if (warp > kW) {
         // ------------------------------------------------------------ loading
-        load_tiles<LOAD, ROWS>(p, s, warp - kW - 1, lane, rank, C, columns, groups, counted, [&](const int round) { return int(p.pl.rounds * C) - 1 - (round * int(C) + int(rank)); },
+        load_tiles<LOAD, RESETS, ROWS>(p, s, warp - kW - 1, lane, rank, C, columns, groups, counted, [&](const int round) { return int(p.pl.rounds * C) - 1 - (round * int(C) + int(rank)); },
                          [&](const int st, const unsigned int g, const unsigned int b, const int tile) {
             const int64_t t0 = int64_t(tile) * ROWS;
             if constexpr (LOAD == kTma) {
@@ -1066,17 +1073,17 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 3
             const int64_t d = int64_t(t.g) * 64 + lane * 2;
             const int64_t t0 = int64_t(t.tile) * ROWS + warp * K;
             const int steps = max(0, min(K, t.rows() - warp * K));
-            const unsigned int fresh = p.reset ? s.fresh[st][warp * K / 32] >> (warp * K % 32) & ((1u << K) - 1u) : 0u;
+            const unsigned int fresh = RESETS ? s.fresh[st][warp * K / 32] >> (warp * K % 32) & ((1u << K) - 1u) : 0u;
             const float2 rt = *reinterpret_cast<const float2 *>(&s.rate[st][lane * 2]);
             T *x = &s.stage[st][0][warp * K][lane * 2], *r = &s.stage[st][1][warp * K][lane * 2], *i = &s.stage[st][2][warp * K][lane * 2];
             const T *dy = &s.stage[st][3][warp * K][lane * 2];
             float2 a[K], h[K], sr[K], si[K], g;
             float4 m;
             float big = 1e30f;
-            if (fresh == 0 && steps == K && __all_sync(0xffffffffu, fmaxf(rt.x, rt.y) < 0.5f && fminf(rt.x, rt.y) > 1e-18f))
-                bwd_steps_of<T, K, true>(x, r, i, dy, rt, fresh, steps, a, h, sr, si, m, g, big);
+            if (steps == K && __all_sync(0xffffffffu, fmaxf(rt.x, rt.y) < 0.5f && fminf(rt.x, rt.y) > 1e-18f))
+                bwd_steps_of<T, K, true, RESETS>(x, r, i, dy, rt, fresh, steps, a, h, sr, si, m, g, big);
             const bool slow = __any_sync(0xffffffffu, big > 60.0f);
-            if (slow) bwd_steps_of<T, K, false>(x, r, i, dy, rt, fresh, steps, a, h, sr, si, m, g, big);
+            if (slow) bwd_steps_of<T, K, false, RESETS>(x, r, i, dy, rt, fresh, steps, a, h, sr, si, m, g, big);
             s.maps[buf][warp][lane] = m;
             s.adj[buf][warp][lane] = g;
             __syncwarp();
@@ -1096,8 +1103,8 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 3
                         store2(r + k * 64, gr);
                         store2(i + k * 64, gi);
                     };
-                    dl = add2(dl, slow ? bwd_grads_of<T, K, false>(x, dy, rt, fresh, steps, a, h, sr, si, hs, gs, out)
-                                       : bwd_grads_of<T, K, true>(x, dy, rt, fresh, steps, a, h, sr, si, hs, gs, out));
+                    dl = add2(dl, slow ? bwd_grads_of<T, K, false, RESETS>(x, dy, rt, fresh, steps, a, h, sr, si, hs, gs, out)
+                                       : bwd_grads_of<T, K, true, RESETS>(x, dy, rt, fresh, steps, a, h, sr, si, hs, gs, out));
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0 && steps > 0) {
@@ -1118,8 +1125,8 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 3
                             if (both) p.dx[q + 1] = Tok<T>::from_f(gx.y), p.dr[q + 1] = Tok<T>::from_f(gr.y), p.di[q + 1] = Tok<T>::from_f(gi.y);
                         }
                     };
-                    dl = add2(dl, slow ? bwd_grads_of<T, K, false>(x, dy, rt, fresh, steps, a, h, sr, si, hs, gs, out)
-                                       : bwd_grads_of<T, K, true>(x, dy, rt, fresh, steps, a, h, sr, si, hs, gs, out));
+                    dl = add2(dl, slow ? bwd_grads_of<T, K, false, RESETS>(x, dy, rt, fresh, steps, a, h, sr, si, hs, gs, out)
+                                       : bwd_grads_of<T, K, true, RESETS>(x, dy, rt, fresh, steps, a, h, sr, si, hs, gs, out));
                 }
                 if (t.more & TileInfo::kLast) {
                     float *q = p.parts + (((int64_t(t.seg()) * C + rank) * kW + warp) * p.s.B + b) * p.s.D + d;
@@ -1282,12 +1289,12 @@ bool make_plan(Plan &pl, Residency &r, const void *kernel, int threads, size_t s
     return true;
 }
 
-template <typename T, int K, Load LOAD, bool LAG>
-ssm_status launch_fwd(FwdArgs<T> p, const Maps3 &tm, bool pairs, cudaStream_t st) {
+template <typename T, int K, Load LOAD, bool LAG, bool RESETS>
+ssm_status launch_fwd_as(FwdArgs<T> p, const Maps3 &tm, bool pairs, cudaStream_t st) {
     static Residency resident;
     constexpr size_t smem = sizeof(FwdShared<T, K, LAG>);
     constexpr int threads = (kW + 1 + kLoaders<LOAD>) * 32;
-    const auto kernel = gated_fwd_kernel<T, K, LOAD, LAG>;
+    const auto kernel = gated_fwd_kernel<T, K, LOAD, LAG, RESETS>;
     const int64_t columns = p.s.B * p.s.groups, n = p.s.B * p.s.D;
     const int segs = max_segs(columns, ceil_div(p.s.L, kChunk));
     if (!make_plan(p.pl, resident, reinterpret_cast<const void *>(kernel), threads, smem, FwdShared<T, K, LAG>::kMaxCluster, columns,
@@ -1313,6 +1320,11 @@ ssm_status launch_fwd(FwdArgs<T> p, const Maps3 &tm, bool pairs, cudaStream_t st
     }
     cudaLaunchKernelEx(&cfg, kernel, p, tm, pairs);
     return launched();
+}
+
+template <typename T, int K, Load LOAD, bool LAG>
+ssm_status launch_fwd(const FwdArgs<T> &p, const Maps3 &tm, bool pairs, cudaStream_t st) {
+    return p.reset ? launch_fwd_as<T, K, LOAD, LAG, true>(p, tm, pairs, st) : launch_fwd_as<T, K, LOAD, LAG, false>(p, tm, pairs, st);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -1374,12 +1386,12 @@ ssm_status run_fwd(const ssm_gated_args *a, cudaStream_t st) {
     return SSM_ERR_UNSUPPORTED;
 }
 
-template <typename T, int K, Load LOAD>
-ssm_status launch_bwd(BwdArgs<T> p, const Maps7 &tm, bool pairs, float *dlam, cudaStream_t st) {
+template <typename T, int K, Load LOAD, bool RESETS>
+ssm_status launch_bwd_as(BwdArgs<T> p, const Maps7 &tm, bool pairs, float *dlam, cudaStream_t st) {
     static Residency resident;
     constexpr size_t smem = sizeof(BwdShared<T, K>);
     constexpr int threads = (kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 32;
-    const auto kernel = gated_bwd_kernel<T, K, LOAD>;
+    const auto kernel = gated_bwd_kernel<T, K, LOAD, RESETS>;
     const int64_t columns = p.s.B * p.s.groups, n = p.s.B * p.s.D;
     const int segs = max_segs(columns, ceil_div(p.s.L, kChunk));
     if (!make_plan(p.pl, resident, reinterpret_cast<const void *>(kernel), threads, smem, BwdShared<T, K>::kMaxCluster, columns,
@@ -1408,6 +1420,11 @@ ssm_status launch_bwd(BwdArgs<T> p, const Maps7 &tm, bool pairs, float *dlam, cu
     gated_dlam_kernel<<<unsigned(ceil_div(p.s.D, 32)), 1024, 0, st>>>(int64_t(p.pl.segs) * p.pl.cluster * kW * p.s.B, p.s.D, p.s.c, p.parts,
                                                                       p.lam, dlam);
     return launched();
+}
+
+template <typename T, int K, Load LOAD>
+ssm_status launch_bwd(const BwdArgs<T> &p, const Maps7 &tm, bool pairs, float *dlam, cudaStream_t st) {
+    return p.reset ? launch_bwd_as<T, K, LOAD, true>(p, tm, pairs, dlam, st) : launch_bwd_as<T, K, LOAD, false>(p, tm, pairs, dlam, st);
 }
 
 template <typename T>
