@@ -687,6 +687,8 @@ class _GatedScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, r, i, lam, h0, reset, c, last):
         ctx.set_materialize_grads(False)
+        if not any(ctx.needs_input_grad):
+            return gated_scan_fwd(x, r, i, lam, h0, reset=reset, c=c, return_last_state=last)
         res = gated_scan_fwd(x, r, i, lam, h0, reset=reset, c=c, return_last_state=last, return_states=True)
         ctx.save_for_backward(x, r, i, lam, reset, res[-1])
         ctx.c, ctx.has_h0 = c, h0 is not None
@@ -805,6 +807,8 @@ class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, residual, eps):
         ctx.set_materialize_grads(False)
+        if not any(ctx.needs_input_grad):
+            return layer_norm_fwd(x, weight, bias, residual, eps=eps)
         res = layer_norm_fwd(x, weight, bias, residual, eps=eps, return_stats=True)
         ctx.save_for_backward(x if residual is None else res[1], weight, res[-2], res[-1])
         ctx.has_bias, ctx.residual, ctx.tok = bias is not None, residual is not None, x.dtype

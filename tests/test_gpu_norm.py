@@ -152,10 +152,25 @@ def test_autograd(ssm, dtype):
     want, bound = ref.layer_norm_bwd(d["dy"], s.detach().cpu(), d["weight"], mean.cpu(), rstd.cpu(), d["dres"])
     for k, n in (("x", "dx"), ("weight", "dweight"), ("bias", "dbias"), ("residual", "dx")):
         ref.check(leaf[k].grad, want[n], bound[n], leaf[k].dtype, k)
+    assert leaf["x"].grad.data_ptr() != leaf["residual"].grad.data_ptr()  # also where the two are equal
     # only the residual stream's gradient arrives: it passes through
     y, s = ssm.layer_norm(*leaf.values())
     gr, gw = torch.autograd.grad(s, (leaf["residual"], leaf["weight"]), g["dres"])
     assert torch.equal(gr, g["dres"]) and torch.equal(gw, torch.zeros_like(gw))
+
+
+def test_no_gradient_asked(ssm):
+    d = cuda(make(5, 64, BF16, 18, True))
+    y, s = ssm.layer_norm(d["x"], d["weight"], d["bias"], d["residual"])
+    assert not y.requires_grad
+    for a, b in zip((y, s), ssm.layer_norm_fwd(d["x"], d["weight"], d["bias"], d["residual"])):
+        assert torch.equal(a, b)
+    x = torch.randn(1, 90, 64, device="cuda", requires_grad=True)
+    lam = torch.zeros(64, device="cuda")
+    with torch.no_grad():
+        y, h = ssm.gated_scan(x, x, x, lam, return_last_state=True)
+    assert not y.requires_grad and torch.equal(h, ssm.gated_scan_fwd(x, x, x, lam, return_last_state=True)[1])
+    assert torch.equal(y, ssm.gated_scan(x, x, x, lam))
 
 
 def test_a_second_derivative_is_refused(ssm):
