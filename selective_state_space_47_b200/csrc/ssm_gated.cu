@@ -303,6 +303,8 @@ struct Maps3 {
 
 constexpr int kFewColumns = 24;  // up to here LAG: 1536 channels of one sequence (575 against 496 us at L=131072)
 
+constexpr int kShort = 32, kShortBack = 16, kManyColumns = 256;  // up to so many tokens of at least so many columns: a thread per channel
+
 enum Load { kTma, kAsync, kPlain };  // 16-byte rows; pieces of 4 or 8 bytes; elements of 2 bytes
 
 // Decays and inputs of a thread's steps, and their map. RESETS: there may be some among them. FAST: every rate
@@ -1200,6 +1202,110 @@ __global__ void __launch_bounds__(128)
     }
 }
 
+// A few tokens of many sequences (a chunk of a decoding batch): a thread walks V neighbouring channels of one
+// sequence through all of them. Tiles would be mostly empty there (B=256 D=5120 bfloat16: 4 tokens 27 against 223 us, 32
+// tokens 104 against 231; from 64 on, 198 against 237, the tiles come level and then ahead: 128 tokens 387 against 260).
+template <typename T, int V>
+__global__ void __launch_bounds__(128) gated_short_kernel(const FwdArgs<T> p) {
+    const int64_t d = (int64_t(blockIdx.x) * 128 + threadIdx.x) * V;
+    if (d >= p.s.D) return;
+    const int L = int(p.s.L);
+    float rt[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) rt[v] = rate(p.lam[d + v], p.s.c);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = 0;
+    for (int64_t b = blockIdx.y; b < p.s.B; b += gridDim.y) {
+        const int64_t o = b * p.s.D + d;
+        const T *x = p.x + b * p.xb + d, *r = p.r + b * p.rb + d, *i = p.i + b * p.ib + d;
+        T *y = p.y + b * p.s.L * p.s.D + d;
+        float h[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            h[v] = p.h0 ? p.h0[o + v] : 0.0f;
+            if (p.states) p.states[o + v] = h[v];  // of the only chunk
+        }
+#pragma unroll 4
+        for (int t = 0; t < L; ++t) {
+            const Vec<T, V> xv = ldv<T, V>(x + t * p.xt), rv = ldv<T, V>(r + t * p.rt), iv = ldv<T, V>(i + t * p.it);
+            const bool fresh = p.reset && p.reset[b * p.s.L + t];
+            Vec<T, V> out;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float e;
+                const float a = decay(rt[v] * sigmoid_f(rv.get(v)), e), sq = e * (2.0f - e), u = sigmoid_f(iv.get(v)) * xv.get(v);
+                h[v] = fresh ? u : fmaf(a, h[v], sq * inv_beta(sq) * u);
+                out.set(v, h[v]);
+            }
+            if (p.y) stv<T, V>(y + t * p.s.D, out);
+        }
+        if (p.h_last)
+#pragma unroll
+            for (int v = 0; v < V; ++v) p.h_last[o + v] = h[v];
+    }
+}
+
+// Its backward: the states before the steps in registers, the tokens read a second time (from the caches) on the way back.
+// A thread's sums of dlam over its sequences are one value of the parts. (B=256 D=5120 bfloat16: 4 tokens 55 against 271 us,
+// 16 tokens 161 against 291; with an array for 32 tokens those cost 275, and 32 tokens 558 against 302.)
+template <typename T, int V>
+__global__ void __launch_bounds__(128) gated_short_bwd_kernel(const BwdArgs<T> p) {
+    const int64_t d = (int64_t(blockIdx.x) * 128 + threadIdx.x) * V;
+    if (d >= p.s.D) return;
+    const int L = int(p.s.L);
+    float rt[V], dl[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) rt[v] = rate(p.lam[d + v], p.s.c), dl[v] = 0.0f;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = 0;
+    for (int64_t b = blockIdx.y; b < p.s.B; b += gridDim.y) {
+        const int64_t o = b * p.s.D + d, first = b * p.s.L * p.s.D + d;
+        const T *x = p.x + b * p.xb + d, *r = p.r + b * p.rb + d, *i = p.i + b * p.ib + d;
+        float h[V], g[V], before[kShortBack][V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = p.states[o + v], g[v] = p.dh_last ? p.dh_last[o + v] : 0.0f;
+#pragma unroll
+        for (int t = 0; t < kShortBack; ++t)
+            if (t < L) {
+                const Vec<T, V> xv = ldv<T, V>(x + t * p.xt), rv = ldv<T, V>(r + t * p.rt), iv = ldv<T, V>(i + t * p.it);
+                const bool fresh = p.reset && p.reset[b * p.s.L + t];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float e;
+                    const float a = decay(rt[v] * sigmoid_f(rv.get(v)), e), sq = e * (2.0f - e), u = sigmoid_f(iv.get(v)) * xv.get(v);
+                    before[t][v] = h[v];
+                    h[v] = fresh ? u : fmaf(a, h[v], sq * inv_beta(sq) * u);
+                }
+            }
+#pragma unroll
+        for (int t = kShortBack - 1; t >= 0; --t)
+            if (t < L) {
+                const Vec<T, V> xv = ldv<T, V>(x + t * p.xt), rv = ldv<T, V>(r + t * p.rt), iv = ldv<T, V>(i + t * p.it),
+                                dv = ldv<T, V>(p.dy + first + t * p.s.D);
+                const bool fresh = p.reset && p.reset[b * p.s.L + t];
+                Vec<T, V> gx, gr, gi;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const float sr = sigmoid_f(rv.get(v)), si = sigmoid_f(iv.get(v)), w = rt[v] * sr, u = si * xv.get(v);
+                    float e;
+                    const float a = decay(w, e), sq = e * (2.0f - e), q = inv_beta(sq), vt = dv.get(v) + g[v];
+                    const float vb = fresh ? vt : vt * (sq * q), dw = fresh ? 0.0f : a * vt * fmaf(a * q, u, -before[t][v]);
+                    gx.set(v, vb * si);
+                    gi.set(v, vb * u * (1.0f - si));
+                    gr.set(v, dw * w * (1.0f - sr));
+                    dl[v] = fmaf(dw, sr, dl[v]);
+                    g[v] = fresh ? 0.0f : a * vt;
+                }
+                stv<T, V>(p.dx + first + t * p.s.D, gx);
+                stv<T, V>(p.dr + first + t * p.s.D, gr);
+                stv<T, V>(p.di + first + t * p.s.D, gi);
+            }
+        if (p.dh0)
+#pragma unroll
+            for (int v = 0; v < V; ++v) p.dh0[o + v] = g[v];
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) p.parts[int64_t(blockIdx.y) * p.s.D + d + v] = dl[v];
+}
+
 // ---------------------------------------------------------------------- host
 inline bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -1371,6 +1477,19 @@ ssm_status run_fwd(const ssm_gated_args *a, cudaStream_t st) {
     p.y = static_cast<T *>(a->y), p.h_last = a->h_last, p.states = a->states;
     const bool pairs = a->dim % 2 == 0 && even(a->x_stride) && even(a->r_stride) && even(a->i_stride) && aligned(a->x, 2 * es) &&
                        aligned(a->r, 2 * es) && aligned(a->i, 2 * es) && aligned(a->y, 2 * es);
+    if (a->seqlen <= kShort && p.s.B * p.s.groups >= kManyColumns) {
+        p.status = p.counter + 1;
+        const bool four = (a->dim | p.xb | p.xt | p.rb | p.rt | p.ib | p.it) % 4 == 0 && aligned(a->x, 4 * es) && aligned(a->r, 4 * es) &&
+                          aligned(a->i, 4 * es) && aligned(a->y, 4 * es);
+        const dim3 grid(unsigned(ceil_div(a->dim, four ? 512 : pairs ? 256 : 128)), unsigned(std::min<int64_t>(a->batch, 65535)));
+        if (four)
+            gated_short_kernel<T, 4><<<grid, 128, 0, st>>>(p);
+        else if (pairs)
+            gated_short_kernel<T, 2><<<grid, 128, 0, st>>>(p);
+        else
+            gated_short_kernel<T, 1><<<grid, 128, 0, st>>>(p);
+        return launched();
+    }
     const auto maps_of = [&](Maps3 &tm, int rows) {
         return pairs && token_map(&tm.x, a->x, a->dtype, a->batch, a->seqlen, a->dim, a->x_stride, rows) &&
                token_map(&tm.r, a->r, a->dtype, a->batch, a->seqlen, a->dim, a->r_stride, rows) &&
@@ -1443,6 +1562,17 @@ ssm_status run_bwd(const ssm_gated_bwd_args *a, cudaStream_t st) {
     for (const void *q : {a->x, a->r, a->i, a->dy, static_cast<const void *>(a->dx), static_cast<const void *>(a->dr),
                           static_cast<const void *>(a->di)})
         pairs = pairs && aligned(q, 2 * es);
+    if (a->seqlen <= kShortBack && p.s.B * p.s.groups >= kManyColumns) {
+        p.status = p.counter + 1;
+        p.parts = reinterpret_cast<float *>(static_cast<unsigned char *>(a->workspace) + carry_bytes(p.s.B, p.s.L, p.s.D));
+        const dim3 grid(unsigned(ceil_div(a->dim, pairs ? 256 : 128)), unsigned(std::min<int64_t>(a->batch, 2048)));  // a row of the parts each
+        if (pairs)
+            gated_short_bwd_kernel<T, 2><<<grid, 128, 0, st>>>(p);
+        else
+            gated_short_bwd_kernel<T, 1><<<grid, 128, 0, st>>>(p);
+        gated_dlam_kernel<<<unsigned(ceil_div(p.s.D, 32)), 1024, 0, st>>>(grid.y, p.s.D, p.s.c, p.parts, p.lam, a->dlam);
+        return launched();
+    }
     constexpr int K = kChunk / kW;
     const int64_t whole[2] = {a->seqlen * a->dim, a->dim};
     const auto map = [&](CUtensorMap &m, const void *q, const int64_t *stride, int rows) {

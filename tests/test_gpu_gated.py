@@ -114,6 +114,59 @@ def test_strided_and_misaligned_tokens(ssm, dtype):
     check_bwd(ssm, d2, g2, dtype, states)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,L,D", [(256, 1, 64), (300, 4, 70), (64, 16, 260), (257, 31, 65), (256, 32, 12), (256, 33, 12), (2500, 3, 8),
+                                   (52, 7, 321)])
+def test_a_few_tokens_of_many_sequences(ssm, B, L, D, dtype):
+    for extras in (False, True):
+        d = make(B, L, D, dtype, seed=B + L, h0=extras, reset=0.1 if extras else 0.0, slow=not extras)
+        g = cuda(d)
+        if extras:  # slices of one projection
+            both = torch.cat([g["r"], g["i"]], 2)
+            g["r"], g["i"] = both[:, :, :D], both[:, :, D:]
+        _, (_, _, states) = check_fwd(ssm, d, g, dtype)
+        got = check_bwd(ssm, d, g, dtype, states)
+        again = ssm.gated_scan_bwd(*(g[k] for k in ("x", "r", "i", "lam", "dy", "h0", "dh_last")), reset=g["reset"])
+        for k in got:
+            assert torch.equal(got[k], again[k]), k
+
+
+def test_a_few_tokens_at_the_gates_ends(ssm):
+    """As the long sequences: tiny rates keep their weight, a closed gate holds the state exactly with finite
+    gradients, and a reset keeps an infinity of the state before it out of what follows."""
+    B, L, D = 300, 9, 12
+    d = make(B, L, D, torch.float32, seed=6, h0=True)
+    d["lam"] = torch.linspace(-60, -8, D)
+    g = cuda(d)
+    _, (_, _, states) = check_fwd(ssm, d, g, torch.float32)
+    check_bwd(ssm, d, g, torch.float32, states)
+    d["r"][:] = float("-inf")
+    g = cuda(d)
+    y, h, states = ssm.gated_scan_fwd(*(g[k] for k in FWD), return_last_state=True, return_states=True)
+    assert torch.equal(y, g["h0"][:, None].expand(-1, L, -1)) and torch.equal(h, g["h0"])
+    got = ssm.gated_scan_bwd(g["x"], g["r"], g["i"], g["lam"], g["dy"], None, g["dh_last"], states=states)
+    for k in ("dx", "dr", "di", "dlam"):
+        assert torch.equal(got[k], torch.zeros_like(got[k])), k
+    d = make(B, L, D, torch.float32, seed=9, h0=True)
+    d["reset"] = torch.zeros(B, L, dtype=torch.bool)
+    d["reset"][:, 4] = True
+    bad = {k: None if v is None else v.clone() for k, v in d.items()}
+    bad["h0"][0] = float("inf")
+    bad["x"][1, 2] = float("nan")
+    bad["dy"][2, 6] = float("nan")
+    g = cuda(bad)
+    y, states = ssm.gated_scan_fwd(*(g[k] for k in FWD), reset=g["reset"], return_states=True)
+    want, bound = ref.gated_scan(*(d[k] for k in FWD), reset=d["reset"])
+    ref.check(y[:, 4:], want[:, 4:], bound[:, 4:], what="y after the reset")
+    ref.check(y[2:], want[2:], bound[2:], what="y")
+    got = ssm.gated_scan_bwd(g["x"], g["r"], g["i"], g["lam"], g["dy"], None, g["dh_last"], states=states, reset=g["reset"])
+    want, bound = ref.gated_scan_bwd(*(d[k] for k in ("x", "r", "i", "lam", "dy", "h0", "dh_last")), reset=d["reset"])
+    for k in ("dx", "dr", "di"):
+        ref.check(got[k][:2, 4:], want[k][:2, 4:], bound[k][:2, 4:], what=k)
+        ref.check(got[k][2, :4], want[k][2, :4], bound[k][2, :4], what=k)
+        ref.check(got[k][3:], want[k][3:], bound[k][3:], what=k)
+
+
 def test_long_sequences(ssm):
     """Many tiles in a row: a few channels over 40000 steps, and several groups of channels."""
     for B, L, D, dtype in ((1, 40000, 3, torch.float32), (2, 9000, 130, torch.bfloat16)):
