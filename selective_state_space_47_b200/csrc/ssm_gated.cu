@@ -196,6 +196,17 @@ __device__ __forceinline__ float rsqrt_approx(float v) {
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+// The largest of three. NAN_WINS: a NaN among them is the result; else it is passed over.
+template <bool NAN_WINS>
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    if constexpr (NAN_WINS) {
+        float r;
+        asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+        return r;
+    } else {
+        return fmaxf(fmaxf(a, b), c);
+    }
+}
 __device__ __forceinline__ float2 load2(const float *p) { return *reinterpret_cast<const float2 *>(p); }
 __device__ __forceinline__ float2 load2(const __nv_bfloat16 *p) {
     const uint32_t w = *reinterpret_cast<const uint32_t *>(p);
@@ -310,7 +321,8 @@ enum Load { kTma, kAsync, kPlain };  // 16-byte rows; pieces of 4 or 8 bytes; el
 // Decays and inputs of a thread's steps, and their map. RESETS: there may be some among them. FAST: every rate
 // between 1e-18 and 1/2 (neither the decay's exponential nor a case for beta = 0 is
 // needed), and one reciprocal serves both sigmoids: 1/(1+E) = (1+F)/((1+E)(1+F)); `big`
-// tells of gates below -41, whose exponentials' product could overflow and w underflow.
+// tells of gates below -41, whose exponentials' product could overflow and w underflow, and (a NaN itself) of a NaN
+// among them where there are resets: r is not used at a reset, and the reciprocal would carry its NaN to the input.
 template <typename T, int K, bool FAST, bool RESETS>
 __device__ __forceinline__ float4 fwd_steps_of(const T *x, const T *r, const T *i, const float2 rt, const unsigned int fresh,
                                                float2 (&a)[K], float2 (&h)[K], float &big) {
@@ -321,7 +333,7 @@ __device__ __forceinline__ float4 fwd_steps_of(const T *x, const T *r, const T *
         float2 sr, si, e;
         if constexpr (FAST) {
             const float2 tr = mul2(load2(r + k * 64), two(-kLog2e)), ti = mul2(load2(i + k * 64), two(-kLog2e));
-            top = fmaxf(fmaxf(top, fmaxf(tr.x, tr.y)), fmaxf(ti.x, ti.y));
+            top = max3<RESETS>(max3<RESETS>(top, tr.x, tr.y), ti.x, ti.y);
             const float2 fr = add2(two(1.0f), make_float2(ex2_approx(tr.x), ex2_approx(tr.y)));
             const float2 fi = add2(two(1.0f), make_float2(ex2_approx(ti.x), ex2_approx(ti.y)));
             const float2 pr = mul2(fr, fi), rc = make_float2(rcp_approx(pr.x), rcp_approx(pr.y));
@@ -713,7 +725,7 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD>) * 32, LAG ? 1 : 2)
             if (__all_sync(0xffffffffu, fmaxf(rt.x, rt.y) < 0.5f && fminf(rt.x, rt.y) > 1e-18f))
                 m = !RESETS || fresh == 0 ? fwd_steps_of<T, K, true, false>(x, r, i, rt, 0u, a, h, big)
                                           : fwd_steps_of<T, K, true, RESETS>(x, r, i, rt, fresh, a, h, big);
-            if (__any_sync(0xffffffffu, big > 60.0f)) m = fwd_steps_of<T, K, false, RESETS>(x, r, i, rt, fresh, a, h, big);
+            if (__any_sync(0xffffffffu, !(big <= 60.0f))) m = fwd_steps_of<T, K, false, RESETS>(x, r, i, rt, fresh, a, h, big);
             s.maps[it & 1][warp][lane] = m;
             __syncwarp();
             if (lane == 0) {
@@ -854,7 +866,7 @@ __device__ __forceinline__ void bwd_steps_of(const T *x, const T *r, const T *i,
         float2 e;
         if constexpr (FAST) {
             const float2 tr = mul2(load2(r + k * 64), two(-kLog2e)), ti = mul2(load2(i + k * 64), two(-kLog2e));
-            top = fmaxf(fmaxf(top, fmaxf(tr.x, tr.y)), fmaxf(ti.x, ti.y));
+            top = max3<RESETS>(max3<RESETS>(top, tr.x, tr.y), ti.x, ti.y);
             const float2 fr = add2(two(1.0f), make_float2(ex2_approx(tr.x), ex2_approx(tr.y)));
             const float2 fi = add2(two(1.0f), make_float2(ex2_approx(ti.x), ex2_approx(ti.y)));
             const float2 pr = mul2(fr, fi), rc = make_float2(rcp_approx(pr.x), rcp_approx(pr.y));
@@ -873,6 +885,7 @@ __device__ __forceinline__ void bwd_steps_of(const T *x, const T *r, const T *i,
             h[k] = mul2(make_float2(sqrt_approx(sq.x), sqrt_approx(sq.y)), u);
         const bool fr = RESETS && (fresh >> k & 1);
         if (fr) h[k] = u;
+        if (!FAST && fr) sr[k] = two(0.0f);  // (a NaN there reaches no gradient)
         if (!FAST && k >= steps) a[k] = two(1.0f);
         P = mul2(P, a[k]);
         H = fr ? h[k] : fma2(a[k], H, h[k]);
@@ -1084,7 +1097,7 @@ __global__ void __launch_bounds__((kW + 1 + kLoaders<LOAD, true, sizeof(T)>) * 3
             float big = 1e30f;
             if (steps == K && __all_sync(0xffffffffu, fmaxf(rt.x, rt.y) < 0.5f && fminf(rt.x, rt.y) > 1e-18f))
                 bwd_steps_of<T, K, true, RESETS>(x, r, i, dy, rt, fresh, steps, a, h, sr, si, m, g, big);
-            const bool slow = __any_sync(0xffffffffu, big > 60.0f);
+            const bool slow = __any_sync(0xffffffffu, !(big <= 60.0f));
             if (slow) bwd_steps_of<T, K, false, RESETS>(x, r, i, dy, rt, fresh, steps, a, h, sr, si, m, g, big);
             s.maps[buf][warp][lane] = m;
             s.adj[buf][warp][lane] = g;
@@ -1290,8 +1303,8 @@ __global__ void __launch_bounds__(128) gated_short_bwd_kernel(const BwdArgs<T> p
                     const float vb = fresh ? vt : vt * (sq * q), dw = fresh ? 0.0f : a * vt * fmaf(a * q, u, -before[t][v]);
                     gx.set(v, vb * si);
                     gi.set(v, vb * u * (1.0f - si));
-                    gr.set(v, dw * w * (1.0f - sr));
-                    dl[v] = fmaf(dw, sr, dl[v]);
+                    gr.set(v, fresh ? 0.0f : dw * w * (1.0f - sr));  // (r, not used at a reset, may be NaN)
+                    if (!fresh) dl[v] = fmaf(dw, sr, dl[v]);
                     g[v] = fresh ? 0.0f : a * vt;
                 }
                 stv<T, V>(p.dx + first + t * p.s.D, gx);

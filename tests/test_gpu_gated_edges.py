@@ -1,0 +1,46 @@
+"""GPU checks of the gated linear recurrence where a value that the formulas never use is NaN,
+and in the forms that other sizes than the plain tests' reach."""
+import pytest
+import torch
+
+from tests import operators_ref as ref
+from tests.conftest import cuda_available
+from tests.test_gpu_gated import FWD, cuda, make
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+BWD = ("x", "r", "i", "lam", "dy", "h0", "dh_last")
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module")
+def ssm():
+    if not cuda_available():
+        pytest.skip("needs a CUDA device")
+    import selective_state_space_47_b200 as m
+    return m
+
+
+# whole tiles by TMA, rows in pieces, odd rows, two passes over few columns, a few tokens by threads
+FORMS = [(2, 400, 64), (2, 400, 34), (2, 400, 33), (1, 5000, 72), (300, 9, 12), (300, 9, 7)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("slow", [True, False], ids=["rates_small", "rates_any"])
+@pytest.mark.parametrize("size", FORMS, ids=lambda s: "x".join(map(str, s)))
+def test_the_decay_gate_is_not_used_at_a_reset(ssm, size, slow, dtype):
+    """At a reset a = 0 and beta = 1 whatever r is: a NaN there reaches no output and no gradient, and dr is 0."""
+    d = make(*size, dtype, seed=11, h0=True, reset=0.05, slow=slow)
+    d["reset"][:, size[1] // 2] = True
+    want, bound = ref.gated_scan(*(d[k] for k in FWD), reset=d["reset"])
+    gw, gb = ref.gated_scan_bwd(*(d[k] for k in BWD), reset=d["reset"])
+    g = cuda(d)
+    g["r"] = g["r"].masked_fill(g["reset"][..., None], NAN)
+    y, h, states = ssm.gated_scan_fwd(*(g[k] for k in FWD), reset=g["reset"], return_last_state=True, return_states=True)
+    ref.check(y, want, bound, dtype, "y")
+    ref.check(h, want[:, -1], bound[:, -1], what="h_last")
+    assert torch.isfinite(states).all()
+    got = ssm.gated_scan_bwd(*(g[k] for k in BWD), states=states, reset=g["reset"])
+    for k in gw:
+        ref.check(got[k], gw[k], gb[k], dtype if k in ("dx", "dr", "di") else F32, k)
+    assert not got["dr"][g["reset"]].any()
