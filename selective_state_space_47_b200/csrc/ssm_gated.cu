@@ -854,7 +854,8 @@ struct Maps7 {
 
 // v_t = dL/dh_t follows v_t = dy_t + a_{t+1} v_{t+1}; with g_t = a_t v_t, what a step hands to
 // the one before it, a piece of time acts on the g entering from its right as g -> P g + G
-// with the forward's P. Steps past the end are the identity.
+// with the forward's P. Steps past the end are the identity. `big` tells of a NaN gate in any case: the adjoint goes by
+// r alone, and the shared reciprocal would carry a NaN of i to it.
 template <typename T, int K, bool FAST, bool RESETS>
 __device__ __forceinline__ void bwd_steps_of(const T *x, const T *r, const T *i, const T *dy, const float2 rt, const unsigned int fresh,
                                              const int steps, float2 (&a)[K], float2 (&h)[K], float2 (&sr)[K], float2 (&si)[K],
@@ -866,7 +867,7 @@ __device__ __forceinline__ void bwd_steps_of(const T *x, const T *r, const T *i,
         float2 e;
         if constexpr (FAST) {
             const float2 tr = mul2(load2(r + k * 64), two(-kLog2e)), ti = mul2(load2(i + k * 64), two(-kLog2e));
-            top = max3<RESETS>(max3<RESETS>(top, tr.x, tr.y), ti.x, ti.y);
+            top = max3<true>(max3<true>(top, tr.x, tr.y), ti.x, ti.y);
             const float2 fr = add2(two(1.0f), make_float2(ex2_approx(tr.x), ex2_approx(tr.y)));
             const float2 fi = add2(two(1.0f), make_float2(ex2_approx(ti.x), ex2_approx(ti.y)));
             const float2 pr = mul2(fr, fi), rc = make_float2(rcp_approx(pr.x), rcp_approx(pr.y));

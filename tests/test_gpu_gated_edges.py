@@ -44,3 +44,27 @@ def test_the_decay_gate_is_not_used_at_a_reset(ssm, size, slow, dtype):
     for k in gw:
         ref.check(got[k], gw[k], gb[k], dtype if k in ("dx", "dr", "di") else F32, k)
     assert not got["dr"][g["reset"]].any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("size", FORMS, ids=lambda s: "x".join(map(str, s)))
+def test_a_bad_input_gate_leaves_the_adjoint(ssm, size, dtype):
+    """A NaN in i spoils the states from its step on, but the adjoint goes by r alone: dx and di are as
+    without it at every other step, and so are dr before it and dh0."""
+    B, L, D = size
+    d = make(B, L, D, dtype, seed=12, h0=True)
+    at = L // 2
+    gw, gb = ref.gated_scan_bwd(*(d[k] for k in BWD))
+    g = cuda(d)
+    g["i"][0, at] = NAN
+    y, states = ssm.gated_scan_fwd(*(g[k] for k in FWD), return_states=True)
+    want, bound = ref.gated_scan(*(d[k] for k in FWD))
+    ref.check(y[0, :at], want[0, :at], bound[0, :at], dtype, "y")
+    assert torch.isnan(y[0, at:]).all()
+    got = ssm.gated_scan_bwd(*(g[k] for k in BWD), states=states)
+    cut = lambda t: torch.cat([t[0, :at], t[0, at + 1:]])
+    for k in ("dx", "di"):
+        ref.check(cut(got[k]), cut(gw[k]), cut(gb[k]), dtype, k)
+        ref.check(got[k][1:], gw[k][1:], gb[k][1:], dtype, k)
+    ref.check(got["dr"][0, :at], gw["dr"][0, :at], gb["dr"][0, :at], dtype, "dr")
+    ref.check(got["dh0"], gw["dh0"], gb["dh0"], what="dh0")
