@@ -485,7 +485,7 @@ class _Launch:
             self.handle = _resolve_stream(stream, dev).cuda_stream
             if self.handle != _raw_stream(index):
                 for t in tensors:
-                    if t is not None:
+                    if isinstance(t, torch.Tensor) and t.is_cuda:  # (what is not is refused inside)
                         t.record_stream(stream)
             self.contexts = (torch.cuda.device(dev), torch.cuda.stream(stream))
 

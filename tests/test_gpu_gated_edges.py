@@ -68,3 +68,20 @@ def test_a_bad_input_gate_leaves_the_adjoint(ssm, size, dtype):
         ref.check(got[k][1:], gw[k][1:], gb[k][1:], dtype, k)
     ref.check(got["dr"][0, :at], gw["dr"][0, :at], gb["dr"][0, :at], dtype, "dr")
     ref.check(got["dh0"], gw["dh0"], gb["dh0"], what="dh0")
+
+
+def test_refusals_on_another_stream(ssm):
+    """Outputs and states elsewhere than on the call's device are refused alike on any stream."""
+    g = cuda(make(2, 70, 8, F32, seed=13, h0=True))
+    args, w = [g[k] for k in FWD], torch.ones(8, device="cuda")
+    here = torch.zeros(2, 70, 8)
+    other = torch.cuda.Stream()
+    for s in (None, other):
+        for bad in (lambda: ssm.gated_scan_fwd(*args, out=here, stream=s),
+                    lambda: ssm.gated_scan_fwd(*args, h_last=here[:, 0], stream=s),
+                    lambda: ssm.gated_scan_bwd(*(g[k] for k in BWD), states=here[:, :2], stream=s),
+                    lambda: ssm.gated_step(*(g[k][:, 0] for k in "xri"), g["lam"], g["h0"], out=here[:, 0], stream=s),
+                    lambda: ssm.layer_norm_fwd(g["x"], w, out=here, stream=s),
+                    lambda: ssm.layer_norm_fwd(g["x"], w, None, g["dy"], residual_out=here, stream=s)):
+            with pytest.raises(ValueError):
+                bad()
