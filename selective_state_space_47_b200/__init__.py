@@ -472,8 +472,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 class _Launch:
     """Where a call's work goes: enters with the stream's handle. Outputs and scratch are allocated
-    inside, so that they belong to that stream; on a caller's stream other than the current one the inputs
-    are held until it has read them."""
+    inside, so that they belong to that stream; on a caller's stream other than the current one the caller's
+    tensors, a workspace among them, are held until it is done with them."""
     __slots__ = ("handle", "contexts")
 
     def __init__(self, dev, stream, tensors):
@@ -485,6 +485,7 @@ class _Launch:
             self.handle = _resolve_stream(stream, dev).cuda_stream
             if self.handle != _raw_stream(index):
                 for t in tensors:
+                    t = t.buf if isinstance(t, ScanWorkspace) else t
                     if isinstance(t, torch.Tensor) and t.is_cuda:  # (what is not is refused inside)
                         t.record_stream(stream)
             self.contexts = (torch.cuda.device(dev), torch.cuda.stream(stream))
@@ -581,7 +582,7 @@ def gated_scan_fwd(x, r, i, lam, h0=None, *, reset=None, c=8.0, return_last_stat
     head = _gated_head(x, r, i, lam, reset, c, h0)
     Bsz, L, Dm = x.shape
     dev, tok, index = x.device, x.dtype, x.get_device()
-    with _Launch(dev, stream, (x, r, i, lam, reset, h0, out, h_last)) as handle:
+    with _Launch(dev, stream, (x, r, i, lam, reset, h0, out, h_last, workspace)) as handle:
         y = torch.empty((Bsz, L, Dm), dtype=tok, device=dev) if out is None else out
         if out is not None:
             _check(y, "out", (Bsz, L, Dm), tok, index)
@@ -611,7 +612,7 @@ def gated_scan_bwd(x, r, i, lam, dy, h0=None, dh_last=None, *, states=None, rese
     _check(dy, "dy", shape, tok, index)
     if dh_last is not None:
         _check(dh_last, "dh_last", (Bsz, Dm), torch.float32, index)
-    with _Launch(dev, stream, (x, r, i, lam, reset, h0, dy, dh_last, states)) as handle:
+    with _Launch(dev, stream, (x, r, i, lam, reset, h0, dy, dh_last, states, workspace)) as handle:
         if states is None:
             states = _gated_states(Bsz, L, Dm, dev)
             _gated_fwd(head, h0, None, None, states, None, dev, handle)
@@ -781,7 +782,7 @@ def layer_norm_bwd(dy, s, weight, mean, rstd, dresidual_out=None, *, residual=Fa
         if not residual:
             raise ValueError("dresidual_out needs residual")
         _check(dresidual_out, "dresidual_out", shape, f32, index)
-    with _Launch(dev, stream, (dy, s, weight, mean, rstd, dresidual_out)) as handle:
+    with _Launch(dev, stream, (dy, s, weight, mean, rstd, dresidual_out, workspace)) as handle:
         dx, dweight, dbias, dres = _norm_bwd(rows, Dm, dy, s, weight, mean, rstd, dresidual_out, residual, bias, workspace, handle)
     return dict(dx=dx, dweight=dweight, dbias=dbias, dresidual=dres)
 

@@ -85,3 +85,32 @@ def test_refusals_on_another_stream(ssm):
                     lambda: ssm.layer_norm_fwd(g["x"], w, None, g["dy"], residual_out=here, stream=s)):
             with pytest.raises(ValueError):
                 bad()
+
+
+@pytest.mark.parametrize("kind", ["tensor", "ScanWorkspace"])
+def test_a_workspace_is_held_on_another_stream(ssm, kind):
+    """A caller's workspace dropped right after a call on another stream is not handed out again before that call has run."""
+    g = cuda(make(2, 600, 96, F32, seed=14, h0=True))
+    args, grads, w = [g[k] for k in FWD], [g[k] for k in BWD], torch.ones(96, device="cuda")
+    _, states = ssm.gated_scan_fwd(*args, return_states=True)
+    _, mean, rstd = ssm.layer_norm_fwd(g["x"], w, return_stats=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for call in (lambda ws: ssm.gated_scan_fwd(*args, workspace=ws, stream=s),
+                 lambda ws: ssm.gated_scan_bwd(*grads, states=states, workspace=ws, stream=s),
+                 lambda ws: ssm.layer_norm_bwd(g["x"], g["x"], w, mean, rstd, workspace=ws, stream=s)):
+        buf = torch.empty(5 << 20, dtype=torch.uint8, device="cuda")
+        at, ws = buf.data_ptr(), buf
+        if kind == "ScanWorkspace":
+            ws = ssm.ScanWorkspace()
+            ws.buf = buf
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(200_000_000)  # about 0.1 s
+        out = call(ws)
+        del buf, ws
+        again = torch.empty(5 << 20, dtype=torch.uint8, device="cuda")
+        busy = not s.query()
+        torch.cuda.synchronize()
+        assert busy and again.data_ptr() != at
+        del out, again
