@@ -409,9 +409,9 @@ ssm_status ssm_ssd_fwd(const ssm_ssd_args *args, void *stream);
  * states (optional output) receives what the backward needs of the forward: the state
  * before every SSM_GATED_CHUNK-th step, [B, ceil(L / SSM_GATED_CHUNK), D] float32
  * (ssm_gated_states_size() bytes). y may be NULL when states or h_last is wanted only.
- * L == 0 writes h_last = h0 (or 0). Outputs must not alias inputs.
- * Errors: SSM_ERR_INVALID for sizes or strides below zero, c not positive and finite,
- * missing pointers, unknown dtype or flags, a short workspace; SSM_ERR_UNSUPPORTED for
+ * L == 0 writes h_last = h0 (or 0). Errors: SSM_ERR_INVALID for sizes or strides below zero,
+ * c not positive and finite, missing pointers, an output that overlaps an input (between a
+ * strided input's first and last element), unknown dtype or flags, a short workspace; SSM_ERR_UNSUPPORTED for
  * misaligned pointers and sizes beyond 2^56 elements or 2^31 tiles.
  */
 #define SSM_GATED_CHUNK 64

@@ -577,7 +577,7 @@ def gated_scan_fwd(x, r, i, lam, h0=None, *, reset=None, c=8.0, return_last_stat
     bool, true where a new document begins (the state before it is dropped and the input is
     taken in full). Returns y [B, L, D] in x's dtype, then with return_last_state the final state
     [B, D] float32, and with return_states the states that gated_scan_bwd takes
-    ([B, ceil(L / 64), D] float32).
+    ([B, ceil(L / 64), D] float32). Outputs (out, h_last) that overlap an input are refused.
     """
     head = _gated_head(x, r, i, lam, reset, c, h0)
     Bsz, L, Dm = x.shape

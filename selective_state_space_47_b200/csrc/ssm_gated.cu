@@ -25,6 +25,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 
 #include "../../include/ssm_scan.h"
 #include "ssm_device.cuh"
@@ -1643,6 +1644,26 @@ bool strides_fit(const A *a) {
     return true;
 }
 
+// A piece of memory that a call reads or writes.
+struct Span {
+    const void *at;
+    size_t bytes;
+};
+template <typename A>
+Span tokens_of(const A *a, const void *q, const int64_t *stride) {  // (strides_fit holds)
+    return {q, size_t((a->batch - 1) * stride[0] + (a->seqlen - 1) * stride[1] + a->dim) * (a->dtype == SSM_BF16 ? 2 : 4)};
+}
+// True where no output overlaps an input. (A block of a cluster may still read the state or adjoint that a sequence
+// starts from when another has written its last.)
+bool apart(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+    for (const Span &o : outputs)
+        for (const Span &i : inputs) {
+            const uintptr_t p = reinterpret_cast<uintptr_t>(o.at), q = reinterpret_cast<uintptr_t>(i.at);
+            if (p && q && p < q + i.bytes && q < p + o.bytes) return false;
+        }
+    return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1679,6 +1700,11 @@ ssm_status ssm_gated_scan_fwd(const ssm_gated_args *args, void *stream) {
                                     : cudaMemsetAsync(a->h_last, 0, nb, st);
         return e == cudaSuccess ? SSM_OK : SSM_ERR_CUDA;
     }
+    const size_t row = size_t(a->dim) * 4, state = size_t(a->batch) * row, steps = size_t(a->batch) * size_t(a->seqlen);
+    if (!apart({{a->y, steps * size_t(a->dim) * es}, {a->h_last, state}, {a->states, ssm_gated_states_size(a->batch, a->seqlen, a->dim)}},
+               {tokens_of(a, a->x, a->x_stride), tokens_of(a, a->r, a->r_stride), tokens_of(a, a->i, a->i_stride), {a->reset, steps},
+                {a->lam, row}, {a->h0, state}}))
+        return SSM_ERR_INVALID;
     if (!a->workspace || a->workspace_bytes < ssm_gated_scan_workspace_size(a)) return SSM_ERR_INVALID;
     if (!aligned(a->workspace, 16)) return SSM_ERR_UNSUPPORTED;
     return a->dtype == SSM_BF16 ? run_fwd<__nv_bfloat16>(a, st) : run_fwd<float>(a, st);
@@ -1721,6 +1747,12 @@ ssm_status ssm_gated_scan_bwd(const ssm_gated_bwd_args *args, void *stream) {
         }
         return launched();
     }
+    const size_t row = size_t(a->dim) * 4, state = size_t(a->batch) * row, steps = size_t(a->batch) * size_t(a->seqlen);
+    const size_t tokens = steps * size_t(a->dim) * es;
+    if (!apart({{a->dx, tokens}, {a->dr, tokens}, {a->di, tokens}, {a->dlam, row}, {a->dh0, state}},
+               {tokens_of(a, a->x, a->x_stride), tokens_of(a, a->r, a->r_stride), tokens_of(a, a->i, a->i_stride), {a->reset, steps},
+                {a->lam, row}, {a->states, ssm_gated_states_size(a->batch, a->seqlen, a->dim)}, {a->dy, tokens}, {a->dh_last, state}}))
+        return SSM_ERR_INVALID;
     if (!a->workspace || a->workspace_bytes < ssm_gated_scan_bwd_workspace_size(a)) return SSM_ERR_INVALID;
     if (!aligned(a->workspace, 16)) return SSM_ERR_UNSUPPORTED;
     return a->dtype == SSM_BF16 ? run_bwd<__nv_bfloat16>(a, st) : run_bwd<float>(a, st);
@@ -1751,6 +1783,8 @@ ssm_status ssm_gated_step(int64_t batch, int64_t dim, ssm_dtype dtype, float c, 
         int64_t m;
         if (__builtin_mul_overflow(batch, s, &m) || m > (int64_t(1) << 56)) return SSM_ERR_UNSUPPORTED;
     }
+    const size_t state = size_t(batch) * size_t(dim) * 4;
+    if (h_out != h && !apart({{h_out, state}}, {{h, state}})) return SSM_ERR_INVALID;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // as many sequences a thread as leave about a thousand threads to each of 148 SMs
     const int64_t across = ceil_div(dim, v);

@@ -91,6 +91,18 @@ def test_gated_scan_bwd_refuses(lib, bad, code):
     assert lib.ssm_gated_scan_bwd(None, None) == INVALID
 
 
+def test_overlapping_arrays_are_refused(lib):
+    """An output over an input: h_last where h0 lies, y over the tokens or the gap of a strided input, a state half over another."""
+    at = lambda k: FAKE + (k << 16)  # of the k-th array
+    for bad in (dict(h_last=at(5)), dict(y=at(0)), dict(y=at(2) + 64), dict(states=at(5) + 128), dict(h_last=at(4)),
+                dict(states=at(3)), dict(batch=2, x_stride=(1 << 20, 32), y=at(0) + (1 << 20))):
+        assert lib.ssm_gated_scan_fwd(ctypes.byref(_gated(**bad)), None) == INVALID, bad
+    for bad in (dict(dh0=at(7)), dict(dx=at(6)), dict(di=at(1) + 32), dict(dlam=at(4)), dict(dh0=at(5) + 64)):
+        assert lib.ssm_gated_scan_bwd(ctypes.byref(_gated(True, **bad)), None) == INVALID, bad
+    step = lambda h, h_out: lib.ssm_gated_step(2, 32, 1, 8.0, at(0), 32, at(1), 32, at(2), 32, at(3), h, h_out, at(6), None)
+    assert step(at(4), at(4) + 128) == INVALID and step(at(4) + 252, at(4)) == INVALID
+
+
 def test_gated_sizes_and_empty_calls(lib):
     assert lib.ssm_gated_states_size(2, 200, 32) == 2 * 4 * 32 * 4
     assert lib.ssm_gated_states_size(2, 0, 32) == 0
