@@ -37,6 +37,7 @@ namespace {
 constexpr int kChunk = SSM_GATED_CHUNK;  // steps between the states kept for the backward
 constexpr int kW = 8;                    // computing warps of a block
 constexpr size_t kWsHeader = 256;
+constexpr int kMostBlocks = 16;          // of a cluster
 
 // ------------------------------------------------------------- element math
 __device__ __forceinline__ float sigmoid_f(float v) { return rcp_approx(1.0f + ex2_approx(-v * kLog2e)); }
@@ -297,7 +298,7 @@ struct alignas(16) TileInfo {
 template <typename T, int K, bool LAG>
 struct FwdShared {
     static constexpr int kStages = LAG ? 3 : 2;
-    static constexpr int kMaxCluster = LAG || sizeof(T) * K <= 16 ? 16 : 8;  // (two blocks fit an SM without LAG)
+    static constexpr int kMaxCluster = LAG || sizeof(T) * K <= 16 ? kMostBlocks : 8;  // (two blocks fit an SM without LAG)
     T stage[kStages][3][kW * K][64];       // x, r, i of a tile
     float4 maps[2][kW][32];                // a warp's map (P, H of a lane's two channels), then its start
     float4 inbox[2][kMaxCluster][32];      // the blocks' maps of a round, from the whole cluster
@@ -836,7 +837,7 @@ struct BwdArgs {
 template <typename T, int K>
 struct BwdShared {
     static constexpr int kStages = 2;
-    static constexpr int kMaxCluster = 16;
+    static constexpr int kMaxCluster = kMostBlocks;
     T stage[kStages][4][kW * K][64];  // x, r, i, dy of a tile; then dx, dr, di in the first three
     float4 maps[2][kW][32];           // a warp's map of the state, then its start: h and g of a lane's two channels
     float2 adj[2][kW][32];            // H of its map of the adjoint (P is the same)
@@ -1341,13 +1342,23 @@ ssm_status launched() { return cudaGetLastError() == cudaSuccess ? SSM_OK : SSM_
 // Segments a column's time may be cut into: enough to deal the columns out evenly.
 int max_segs(int64_t columns, int64_t chunks) { return int(std::max<int64_t>(1, std::min<int64_t>(chunks, std::max<int64_t>(8, std::min<int64_t>(256, 4096 / columns))))); }
 
-// Segments times blocks of a cluster: what each column's sums of dlam are spread over at most.
-int most_parts(int64_t columns) { return int(std::max<int64_t>(16, std::min<int64_t>(256, 4096 / columns))); }
+// Segments times blocks of a cluster: what each column's sums of dlam are spread over at most. No plan has a
+// cluster with twice as many blocks as there are tiles, nor more segments than rounds.
+int most_parts(int64_t columns, int64_t tiles) {
+    int64_t n = 1;
+    for (int64_t c = 1; c <= kMostBlocks && (c == 1 || c / 2 < tiles); c *= 2) n = std::max(n, c * ceil_div(tiles, c));
+    return int(std::min(n, std::max<int64_t>(kMostBlocks, std::min<int64_t>(256, 4096 / columns))));
+}
 
+// The header, and what segments hand on: nothing where the time is one segment.
 size_t carry_bytes(int64_t B, int64_t L, int64_t D) {
     const int64_t segs = max_segs(B * ceil_div(D, 64), ceil_div(L, kChunk));
-    return kWsHeader + 2 * up256(size_t(B) * size_t(D) * size_t(segs) * 8);
+    return kWsHeader + (segs > 1 ? 2 * up256(size_t(B) * size_t(D) * size_t(segs) * 8) : 0);
 }
+
+// Whether a call takes the few-token kernels: the forward up to kShort tokens, the backward up to kShortBack.
+bool few_tokens(int64_t B, int64_t L, int64_t D, int most) { return L <= most && B * ceil_div(D, 64) >= kManyColumns; }
+int64_t short_rows(int64_t B) { return std::min<int64_t>(B, 2048); }  // of their backward's blocks, each a row of the parts
 
 // Clusters of each size that the GPU holds at once (0: not asked yet), by device.
 struct Residency {
@@ -1401,7 +1412,7 @@ bool make_plan(Plan &pl, Residency &r, const void *kernel, int threads, size_t s
         const double per = 1.0 + 0.03 * k;
         consider(rounds, false, double(ceil_div(columns, n)) * double(rounds) * per);
         for (int64_t segs = 2; segs <= std::min<int64_t>(most_segs, rounds); segs += std::max<int64_t>(1, segs / 4)) {
-            if (segs * c > most_parts(columns)) break;
+            if (segs * c > most_parts(columns, tiles)) break;
             const int64_t iters = ceil_div(rounds, segs), items = columns * ceil_div(rounds, iters);
             if (columns >= n) consider(iters, false, double(ceil_div(items, n)) * double(iters) * per + 1.0);
             if (c == 1) consider(iters, true, 2.0 * double(ceil_div(items, n)) * double(iters) + 6.0);
@@ -1492,7 +1503,7 @@ ssm_status run_fwd(const ssm_gated_args *a, cudaStream_t st) {
     p.y = static_cast<T *>(a->y), p.h_last = a->h_last, p.states = a->states;
     const bool pairs = a->dim % 2 == 0 && even(a->x_stride) && even(a->r_stride) && even(a->i_stride) && aligned(a->x, 2 * es) &&
                        aligned(a->r, 2 * es) && aligned(a->i, 2 * es) && aligned(a->y, 2 * es);
-    if (a->seqlen <= kShort && p.s.B * p.s.groups >= kManyColumns) {
+    if (few_tokens(a->batch, a->seqlen, a->dim, kShort)) {
         p.status = p.counter + 1;
         const bool four = (a->dim | p.xb | p.xt | p.rb | p.rt | p.ib | p.it) % 4 == 0 && aligned(a->x, 4 * es) && aligned(a->r, 4 * es) &&
                           aligned(a->i, 4 * es) && aligned(a->y, 4 * es);
@@ -1577,10 +1588,10 @@ ssm_status run_bwd(const ssm_gated_bwd_args *a, cudaStream_t st) {
     for (const void *q : {a->x, a->r, a->i, a->dy, static_cast<const void *>(a->dx), static_cast<const void *>(a->dr),
                           static_cast<const void *>(a->di)})
         pairs = pairs && aligned(q, 2 * es);
-    if (a->seqlen <= kShortBack && p.s.B * p.s.groups >= kManyColumns) {
+    if (few_tokens(a->batch, a->seqlen, a->dim, kShortBack)) {
         p.status = p.counter + 1;
-        p.parts = reinterpret_cast<float *>(static_cast<unsigned char *>(a->workspace) + carry_bytes(p.s.B, p.s.L, p.s.D));
-        const dim3 grid(unsigned(ceil_div(a->dim, pairs ? 256 : 128)), unsigned(std::min<int64_t>(a->batch, 2048)));  // a row of the parts each
+        p.parts = reinterpret_cast<float *>(static_cast<unsigned char *>(a->workspace) + kWsHeader);
+        const dim3 grid(unsigned(ceil_div(a->dim, pairs ? 256 : 128)), unsigned(short_rows(a->batch)));
         if (pairs)
             gated_short_bwd_kernel<T, 2><<<grid, 128, 0, st>>>(p);
         else
@@ -1675,7 +1686,8 @@ size_t ssm_gated_states_size(int64_t batch, int64_t seqlen, int64_t dim) {
 
 size_t ssm_gated_scan_workspace_size(const ssm_gated_args *a) {
     if (check_common(a) != SSM_OK) return 0;
-    return (a->batch == 0 || a->dim == 0) ? 0 : carry_bytes(a->batch, a->seqlen, a->dim);
+    if (a->batch == 0 || a->dim == 0) return 0;
+    return few_tokens(a->batch, a->seqlen, a->dim, kShort) ? kWsHeader : carry_bytes(a->batch, a->seqlen, a->dim);
 }
 
 ssm_status ssm_gated_scan_fwd(const ssm_gated_args *args, void *stream) {
@@ -1713,9 +1725,9 @@ ssm_status ssm_gated_scan_fwd(const ssm_gated_args *args, void *stream) {
 size_t ssm_gated_scan_bwd_workspace_size(const ssm_gated_bwd_args *a) {
     if (check_common(a) != SSM_OK) return 0;
     if (a->batch == 0 || a->dim == 0) return 0;
-    const int64_t columns = a->batch * ceil_div(a->dim, 64);
-    return carry_bytes(a->batch, a->seqlen, a->dim) +
-           size_t(a->batch) * size_t(a->dim) * size_t(most_parts(columns)) * kW * 4;
+    if (few_tokens(a->batch, a->seqlen, a->dim, kShortBack)) return kWsHeader + size_t(short_rows(a->batch)) * size_t(a->dim) * 4;
+    const int parts = most_parts(a->batch * ceil_div(a->dim, 64), ceil_div(a->seqlen, kChunk));
+    return carry_bytes(a->batch, a->seqlen, a->dim) + size_t(a->batch) * size_t(a->dim) * size_t(parts) * kW * 4;
 }
 
 ssm_status ssm_gated_scan_bwd(const ssm_gated_bwd_args *args, void *stream) {

@@ -114,3 +114,37 @@ def test_a_workspace_is_held_on_another_stream(ssm, kind):
         torch.cuda.synchronize()
         assert busy and again.data_ptr() != at
         del out, again
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("size", [(1, 1, 3), (2, 64, 70), (2, 65, 70), (3, 190, 64), (1, 700, 200), (1, 1100, 33), (4, 300, 2048), (40, 130, 600),
+                                  (1, 6000, 5120), (1, 50000, 72), (300, 3, 7), (2500, 16, 8), (300, 30, 64), (300, 64, 64)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_calls_keep_to_their_workspace(ssm, size, dtype):
+    """With exactly the bytes asked for, and whatever they hold, results are as with scratch of the call's own, and what lies behind stays."""
+    import ctypes
+    from selective_state_space_47_b200 import _native
+    B, L, D = size
+    gen = torch.Generator(device="cuda").manual_seed(B + L + D)
+    n = lambda *s: torch.randn(*s, device="cuda", generator=gen)
+    x, r, i, dy = (n(B, L, D).to(dtype) for _ in range(4))
+    lam, h0, dl = n(D) - 3, n(B, D), n(B, D)
+    a, b = _native.GatedArgs(), _native.GatedBwdArgs()
+    for q in (a, b):
+        q.batch, q.seqlen, q.dim, q.dtype, q.c = B, L, D, ssm._TOKEN_DTYPES[dtype], 8.0
+    fore = _native.lib().ssm_gated_scan_workspace_size(ctypes.byref(a))
+    back = _native.lib().ssm_gated_scan_bwd_workspace_size(ctypes.byref(b))
+    def exactly(nbytes):
+        buf = torch.full((nbytes + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        return buf, buf[:nbytes]
+    y, h, st = ssm.gated_scan_fwd(x, r, i, lam, h0, return_last_state=True, return_states=True)
+    buf, ws = exactly(fore)
+    for p, q in zip((y, h, st), ssm.gated_scan_fwd(x, r, i, lam, h0, return_last_state=True, return_states=True, workspace=ws)):
+        assert torch.equal(p, q)
+    assert ssm.workspace_status(ws) == 0 and (buf[fore:] == 0xA5).all()
+    want = ssm.gated_scan_bwd(x, r, i, lam, dy, h0, dl, states=st)
+    buf, ws = exactly(back)
+    got = ssm.gated_scan_bwd(x, r, i, lam, dy, h0, dl, states=st, workspace=ws)
+    for k in want:
+        assert torch.equal(want[k], got[k]), k
+    assert ssm.workspace_status(ws) == 0 and (buf[back:] == 0xA5).all()

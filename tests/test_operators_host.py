@@ -118,6 +118,21 @@ def test_gated_sizes_and_empty_calls(lib):
     assert lib.ssm_gated_scan_fwd(ctypes.byref(_gated(seqlen=0, h_last=None)), None) == OK
 
 
+@pytest.mark.parametrize("B,L,D,most", [(256, 4, 5120, 6 << 20), (2048, 4, 4096, 34 << 20), (70000, 1, 64, 1 << 20), (256, 40, 5120, 43 << 20),
+                                        (2048, 200, 4096, 2 << 30), (1, 64, 64, 1 << 12), (4, 2048, 1536, 10 << 20)])
+def test_gated_workspace_goes_by_the_length(lib, B, L, D, most):
+    """The backward's scratch: a few-token call leaves at most 2048 rows of sums (4 bytes a channel), a call of n tiles of 64
+    steps at most 32 bytes a channel and tile (a cluster's last round rounded up) and, beyond one tile, the segments'
+    16 bytes; the forward's is a part of that. So neither outgrows the tokens."""
+    kw = dict(batch=B, seqlen=L, dim=D, x_stride=(L * D, D), r_stride=(L * D, D), i_stride=(L * D, D))
+    back = lib.ssm_gated_scan_bwd_workspace_size(ctypes.byref(_gated(True, **kw)))
+    fore = lib.ssm_gated_scan_workspace_size(ctypes.byref(_gated(**kw)))
+    assert 256 <= back <= most and 256 <= fore <= back
+    tiles = -(-L // 64)
+    assert back <= 1024 + B * D * (2 * tiles * 32 + 16 * tiles)
+    assert fore <= 1024 + (B * D * 16 * tiles if tiles > 1 else 0)
+
+
 def test_gated_step_refuses(lib):
     def call(batch=2, dim=32, dtype=1, c=8.0, x=FAKE, xs=32, r=FAKE, rs=32, i=FAKE, i_s=32, lam=FAKE, h=FAKE,
              h_out=FAKE, y=FAKE + (1 << 16)):
