@@ -712,6 +712,8 @@ class _GatedScan(torch.autograd.Function):
 def gated_scan(x, r, i, lam, h0=None, *, reset=None, c=8.0, return_last_state=False):
     """The gated linear recurrence with its backward attached for torch.autograd: y (and the
     final state) from gated_scan_fwd; gradients for x, r, i, lam and h0 from gated_scan_bwd."""
+    if not torch.is_grad_enabled():  # (a Function's needs_input_grad goes by the tensors' own flags even then)
+        return gated_scan_fwd(x, r, i, lam, h0, reset=reset, c=c, return_last_state=return_last_state)
     return _GatedScan.apply(x, r, i, lam, h0, reset, c, return_last_state)
 
 
@@ -832,4 +834,6 @@ class _LayerNorm(torch.autograd.Function):
 def layer_norm(x, weight, bias=None, residual=None, *, eps=1e-5):
     """The layer norm with its backward attached for torch.autograd: y, or with a residual
     (y, x + residual), from layer_norm_fwd; gradients from layer_norm_bwd."""
+    if not torch.is_grad_enabled():
+        return layer_norm_fwd(x, weight, bias, residual, eps=eps)
     return _LayerNorm.apply(x, weight, bias, residual, eps)

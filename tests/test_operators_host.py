@@ -255,3 +255,31 @@ def _differences(loss, tensors, grads, eps=1e-6):
             flat[j] = keep
             # truncation eps^2 and cancellation 1e-16 / eps, on values of order 10
             assert abs((up - down).item() / (2 * eps) - gf[j].item()) <= 1e-7 * max(1.0, abs(gf[j].item())), (k, j)
+
+
+@pytest.mark.parametrize("off", [torch.no_grad, torch.inference_mode])
+def test_nothing_is_kept_where_no_graph_is(monkeypatch, off):
+    """With gradients switched off the wrappers ask the kernels for neither states nor statistics, though the parameters
+    require gradients; with a graph they do."""
+    asked = []
+
+    def scan(x, *rest, return_last_state=False, return_states=False, **kw):
+        asked.append(return_states)
+        res = (x + 0.0,) + ((x[:, 0] + 0.0,) if return_last_state else ()) + ((x[:, :1],) if return_states else ())
+        return res if len(res) > 1 else res[0]
+
+    def norm(x, weight, bias=None, residual=None, *, eps=1e-5, return_stats=False):
+        asked.append(return_stats)
+        res = (x + 0.0,) + ((residual + x,) if residual is not None else ()) + ((x[..., 0], x[..., 0]) if return_stats else ())
+        return res if len(res) > 1 else res[0]
+
+    monkeypatch.setattr(ssm, "gated_scan_fwd", scan)
+    monkeypatch.setattr(ssm, "layer_norm_fwd", norm)
+    x, p = torch.randn(2, 3, 4), torch.nn.Parameter(torch.zeros(4))
+    calls = (lambda: ssm.gated_scan(x, x, x, p), lambda: ssm.gated_scan(x, x, x, p, return_last_state=True)[0],
+             lambda: ssm.layer_norm(x, p), lambda: ssm.layer_norm(x, p, p, x)[0])
+    with off():
+        for call in calls:
+            assert not call().requires_grad
+    assert asked == [False] * 4
+    assert all(call().requires_grad for call in calls) and asked[4:] == [True] * 4
