@@ -397,8 +397,9 @@ ssm_status ssm_ssd_fwd(const ssm_ssd_args *args, void *stream);
  * state before it is dropped, whatever it holds. The state and every factor are float32
  * (1 - a_t is formed without cancellation); y is rounded once. Neighbouring pieces of
  * time are combined in an order that depends on the shape, the strides and the GPU alone,
- * so results repeat bit for bit. ssm_workspace_status() reports a bounded device-side wait that
- * gave up (SSM_ERR_TIMEOUT: that call's outputs are not valid), here and in the backward.
+ * so results repeat bit for bit. A bounded device-side wait that gave up, here or in the backward,
+ * leaves SSM_ERR_TIMEOUT for ssm_workspace_status() and, whatever becomes of the workspace, for
+ * ssm_gated_status(): that call's outputs are not valid.
  *
  * x, r, i may be strided: element [b, t, d] of x lies at x + b x_stride[0] + t x_stride[1]
  * + d (strides in elements, not negative; one over a single sequence or step does not count), so
@@ -419,7 +420,9 @@ ssm_status ssm_ssd_fwd(const ssm_ssd_args *args, void *stream);
 typedef struct {
     int64_t batch, seqlen, dim;
     ssm_dtype dtype;         /* of x, r, i, y                                         */
-    uint32_t flags;          /* 0                                                     */
+    uint32_t flags;          /* 0 (or SSM_TEST_DROP_HANDOFF: in calls that cut time into
+                                segments handed on in turn, the first one of the first 64 channels
+                                of sequence 0 is left out)                            */
     float c;                 /* scale of the rate (8 is usual)                        */
     const void *x;           /* [B, L, D] input                                       */
     const void *r;           /* [B, L, D] decay gate, before its sigmoid              */
@@ -454,7 +457,7 @@ ssm_status ssm_gated_scan_fwd(const ssm_gated_args *args, void *stream);
 typedef struct {
     int64_t batch, seqlen, dim;
     ssm_dtype dtype;
-    uint32_t flags;          /* 0                                                     */
+    uint32_t flags;          /* as in the forward                                     */
     float c;
     const void *x, *r, *i;   /* the forward's inputs                                  */
     int64_t x_stride[2], r_stride[2], i_stride[2];
@@ -472,6 +475,14 @@ typedef struct {
 
 size_t ssm_gated_scan_bwd_workspace_size(const ssm_gated_bwd_args *args);
 ssm_status ssm_gated_scan_bwd(const ssm_gated_bwd_args *args, void *stream);
+
+/*
+ * Whether a bounded wait of a gated call on the current device has given up since this was last asked:
+ * SSM_OK or SSM_ERR_TIMEOUT. Synchronises `stream`; calls on other streams count once they are
+ * done. For calls whose workspace is not at hand afterwards (a scratch allocation, an autograd
+ * backward); ssm_workspace_status() tells which call it was. Not to be captured into a graph.
+ */
+ssm_status ssm_gated_status(void *stream);
 
 /*
  * One token of the gated recurrence for every sequence and channel: x, r, i [B, D] with a

@@ -23,7 +23,7 @@ from ._native import SSM_A_GENERAL, SSM_DELTA_SOFTPLUS, SSM_EXACT_ZOH
 
 __all__ = ["scan_fwd", "scan_fwd_host", "scan_bwd", "selective_scan", "ssd_fwd", "step", "workspace_size",
            "workspace_status", "ScanWorkspace", "gated_scan", "gated_scan_fwd", "gated_scan_bwd", "gated_step",
-           "layer_norm", "layer_norm_fwd", "layer_norm_bwd"]
+           "gated_status", "layer_norm", "layer_norm_fwd", "layer_norm_bwd"]
 
 _TOKEN_DTYPES = {torch.float32: _native.SSM_F32, torch.bfloat16: _native.SSM_BF16}
 
@@ -534,7 +534,7 @@ def _scratch(nbytes, workspace, dev):
     return ws
 
 
-def _gated_head(x, r, i, lam, reset, c, h0):
+def _gated_head(x, r, i, lam, reset, c, h0, flags=0):
     """Check what the gated scan's forward and backward take alike: the argument structs' first fields."""
     index, tok, shape = x.get_device(), x.dtype, x.shape
     if tok not in _TOKEN_DTYPES:
@@ -550,7 +550,7 @@ def _gated_head(x, r, i, lam, reset, c, h0):
         _check(reset, "reset", (Bsz, L), torch.bool, index)
     if h0 is not None:
         _check(h0, "h0", (Bsz, Dm), torch.float32, index)
-    return (Bsz, L, Dm, _TOKEN_DTYPES[tok], 0, c, x.data_ptr(), r.data_ptr(), i.data_ptr(), x.stride()[:2], r.stride()[:2],
+    return (Bsz, L, Dm, _TOKEN_DTYPES[tok], flags, c, x.data_ptr(), r.data_ptr(), i.data_ptr(), x.stride()[:2], r.stride()[:2],
             i.stride()[:2], _at(reset), lam.data_ptr())
 
 
@@ -568,7 +568,7 @@ def _gated_fwd(head, h0, y, h_last, states, workspace, dev, handle):
 
 
 def gated_scan_fwd(x, r, i, lam, h0=None, *, reset=None, c=8.0, return_last_state=False, return_states=False,
-                   out=None, h_last=None, workspace=None, stream=None):
+                   out=None, h_last=None, workspace=None, stream=None, _test_flags=0):
     """Gated linear recurrence over whole sequences (see include/ssm_scan.h, ssm_gated_scan_fwd):
     a_t = exp(-c softplus(lam) sigmoid(r_t)), h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t.
 
@@ -577,9 +577,9 @@ def gated_scan_fwd(x, r, i, lam, h0=None, *, reset=None, c=8.0, return_last_stat
     bool, true where a new document begins (the state before it is dropped and the input is
     taken in full). Returns y [B, L, D] in x's dtype, then with return_last_state the final state
     [B, D] float32, and with return_states the states that gated_scan_bwd takes
-    ([B, ceil(L / 64), D] float32). Outputs (out, h_last) that overlap an input are refused.
+    ([B, ceil(L / 64), D] float32). Outputs (out, h_last) that overlap an input are refused. _test_flags: test hooks of the C ABI.
     """
-    head = _gated_head(x, r, i, lam, reset, c, h0)
+    head = _gated_head(x, r, i, lam, reset, c, h0, _test_flags)
     Bsz, L, Dm = x.shape
     dev, tok, index = x.device, x.dtype, x.get_device()
     with _Launch(dev, stream, (x, r, i, lam, reset, h0, out, h_last, workspace)) as handle:
@@ -598,7 +598,7 @@ def gated_scan_fwd(x, r, i, lam, h0=None, *, reset=None, c=8.0, return_last_stat
 
 
 def gated_scan_bwd(x, r, i, lam, dy, h0=None, dh_last=None, *, states=None, reset=None, c=8.0, workspace=None,
-                   stream=None):
+                   stream=None, _test_flags=0):
     """Backward of gated_scan_fwd (see include/ssm_scan.h, ssm_gated_scan_bwd): gradients given
     dy = dL/dy [B, L, D] (dtype of x) and optionally dh_last = dL/dh_L [B, D] float32. states:
     what the forward returned with return_states; without them they are computed again
@@ -606,7 +606,7 @@ def gated_scan_bwd(x, r, i, lam, dy, h0=None, dh_last=None, *, states=None, rese
 
     Returns a dict: dx, dr, di [B, L, D] in x's dtype, dlam [D] and dh0 [B, D] float32.
     """
-    head = _gated_head(x, r, i, lam, reset, c, h0)
+    head = _gated_head(x, r, i, lam, reset, c, h0, _test_flags)
     shape = Bsz, L, Dm = x.shape
     dev, tok, index = x.device, x.dtype, x.get_device()
     _check(dy, "dy", shape, tok, index)
@@ -634,6 +634,22 @@ def _gated_bwd(head, x, states, dy, dh_last, workspace, handle):
     a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
     _native.check(lib.ssm_gated_scan_bwd(ref, handle), "ssm_gated_scan_bwd")
     return dx, dr, di, dlam, dh0
+
+
+def gated_status(device=None, *, stream=None):
+    """Synchronise and return, then forget, whether a bounded wait of a gated call on `device` (default: the current
+    one) has given up since this was last asked: 0, or SSM_ERR_TIMEOUT, and that call's outputs are not valid (see
+    include/ssm_scan.h, ssm_gated_status). Without a workspace of the caller's, as in gated_scan and its backward, this
+    is where a failure shows."""
+    dev = torch.device("cuda" if device is None else device)
+    if dev.type != "cuda":
+        raise ValueError(f"device must be a CUDA device, got {dev}")
+    dev = torch.device("cuda", torch.cuda.current_device() if dev.index is None else dev.index)
+    with _Launch(dev, stream, ()) as handle:
+        code = int(_native.lib().ssm_gated_status(handle))
+    if code not in (_native.SSM_OK, _native.SSM_ERR_TIMEOUT):
+        _native.check(code, "ssm_gated_status")
+    return code
 
 
 def gated_step(x, r, i, lam, h, *, c=8.0, h_out=None, out=None, stream=None):

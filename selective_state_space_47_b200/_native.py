@@ -21,7 +21,7 @@ EXPORTS = ("ssm_scan_workspace_size", "ssm_scan_fwd", "ssm_step", "ssm_step_conv
            "ssm_status_string", "ssm_scan_fwd_noalloc", "ssm_noalloc_status", "ssm_scan_host_staging_size",
            "ssm_scan_fwd_host", "ssm_scan_bwd_workspace_size", "ssm_scan_bwd", "ssm_ssd_workspace_size",
            "ssm_ssd_fwd", "ssm_gated_states_size", "ssm_gated_scan_workspace_size", "ssm_gated_scan_fwd",
-           "ssm_gated_scan_bwd_workspace_size", "ssm_gated_scan_bwd", "ssm_gated_step", "ssm_layer_norm_fwd",
+           "ssm_gated_scan_bwd_workspace_size", "ssm_gated_scan_bwd", "ssm_gated_status", "ssm_gated_step", "ssm_layer_norm_fwd",
            "ssm_layer_norm_bwd_workspace_size", "ssm_layer_norm_bwd")
 
 
@@ -155,6 +155,8 @@ def lib():
         L.ssm_gated_scan_bwd_workspace_size.restype = ctypes.c_size_t
         L.ssm_gated_scan_bwd.argtypes = [ctypes.POINTER(GatedBwdArgs), vp]
         L.ssm_gated_scan_bwd.restype = ctypes.c_int
+        L.ssm_gated_status.argtypes = [vp]
+        L.ssm_gated_status.restype = ctypes.c_int
         L.ssm_gated_step.argtypes = [i64, i64, ctypes.c_int, ctypes.c_float] + [vp, i64] * 3 + [vp] * 5
         L.ssm_gated_step.restype = ctypes.c_int
         L.ssm_layer_norm_fwd.argtypes = [ctypes.POINTER(NormArgs), vp]

@@ -26,6 +26,7 @@
 #include <algorithm>
 #include <atomic>
 #include <initializer_list>
+#include <mutex>
 
 #include "../../include/ssm_scan.h"
 #include "ssm_device.cuh"
@@ -137,6 +138,15 @@ __device__ __forceinline__ void st_word(unsigned long long *p, unsigned long lon
 }
 __device__ __forceinline__ unsigned long long pack(float h) { return (1ull << 32) | __float_as_uint(h); }
 
+// What a wait that gives up leaves behind: the call's status word, which may be in scratch that nobody reads, and a
+// word of the device, which outlives the call (ssm_gated_status takes it).
+__device__ unsigned int gave_up, gave_up_taken;
+__device__ __forceinline__ void give_up(unsigned int *status) {
+    atomicExch(status, unsigned(SSM_ERR_TIMEOUT));
+    atomicExch(&gave_up, unsigned(SSM_ERR_TIMEOUT));
+}
+__global__ void gave_up_take_kernel() { gave_up_taken = atomicExch(&gave_up, 0u); }
+
 // Waits for a word to be written. After 2 s, or once another wait has given up, it sets the
 // status and returns the zero word (the call's outputs are then not valid).
 __device__ __noinline__ unsigned long long wait_slow(const unsigned long long *p, unsigned int *status) {
@@ -147,7 +157,7 @@ __device__ __noinline__ unsigned long long wait_slow(const unsigned long long *p
             if (v != 0) return v;
         }
         if (globaltimer_ns() - t > 2000000000ull || *reinterpret_cast<volatile unsigned int *>(status) != 0) {
-            atomicExch(status, unsigned(SSM_ERR_TIMEOUT));
+            give_up(status);
             return 0;
         }
     }
@@ -240,7 +250,7 @@ __device__ __noinline__ bool wait_phase_slow(uint64_t *bar, uint32_t parity, vol
         if (*abort) return false;
         if (globaltimer_ns() - t > 4000000000ull) {
             *abort = 1;
-            atomicExch(status, unsigned(SSM_ERR_TIMEOUT));
+            give_up(status);
             return false;
         }
     }
@@ -268,6 +278,7 @@ struct Plan {
     int cluster, iters, segs;
     unsigned int items;
     bool local;               // one pass for the segments' maps before the pass that writes
+    bool drop_handoff;        // test hook, seen by the host only
     int grid;
 };
 
@@ -1421,6 +1432,14 @@ bool make_plan(Plan &pl, Residency &r, const void *kernel, int threads, size_t s
     return true;
 }
 
+// Counter, status and hand-off words of a plan whose segments are handed on in turn. Test hook: the counter starts
+// behind the first segment of the first column, so that nobody hands its state on.
+bool clear_words(const Plan &pl, unsigned char *ws, int64_t n, cudaStream_t st) {
+    if (pl.segs == 1 || pl.local) return true;
+    return cudaMemsetAsync(ws, 0, kWsHeader + size_t(n) * size_t(pl.segs) * 8, st) == cudaSuccess &&
+           (!pl.drop_handoff || cudaMemsetAsync(ws, 1, 1, st) == cudaSuccess);
+}
+
 template <typename T, int K, Load LOAD, bool LAG, bool RESETS>
 ssm_status launch_fwd_as(FwdArgs<T> p, const Maps3 &tm, bool pairs, cudaStream_t st) {
     static Residency resident;
@@ -1436,8 +1455,7 @@ ssm_status launch_fwd_as(FwdArgs<T> p, const Maps3 &tm, bool pairs, cudaStream_t
     p.status = p.counter + 1;
     p.starts = reinterpret_cast<unsigned long long *>(ws + kWsHeader);
     Map *maps = reinterpret_cast<Map *>(ws + kWsHeader + up256(size_t(n) * size_t(segs) * 8));
-    if (p.pl.segs > 1 && !p.pl.local && cudaMemsetAsync(ws, 0, kWsHeader + size_t(n) * size_t(p.pl.segs) * 8, st) != cudaSuccess)
-        return SSM_ERR_CUDA;
+    if (!clear_words(p.pl, ws, n, st)) return SSM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(p.pl.grid)), cfg.blockDim = dim3(unsigned(threads)), cfg.dynamicSmemBytes = smem, cfg.stream = st;
     cudaLaunchAttribute at;
@@ -1495,6 +1513,7 @@ ssm_status run_fwd(const ssm_gated_args *a, cudaStream_t st) {
     constexpr size_t es = sizeof(T);
     FwdArgs<T> p = {};
     p.s = {a->batch, a->seqlen, a->dim, ceil_div(a->dim, 64), a->c};
+    p.pl.drop_handoff = (a->flags & SSM_TEST_DROP_HANDOFF) != 0;
     p.counter = static_cast<unsigned int *>(a->workspace);
     p.x = static_cast<const T *>(a->x), p.r = static_cast<const T *>(a->r), p.i = static_cast<const T *>(a->i);
     p.xb = a->x_stride[0], p.xt = a->x_stride[1], p.rb = a->r_stride[0], p.rt = a->r_stride[1];
@@ -1547,8 +1566,7 @@ ssm_status launch_bwd_as(BwdArgs<T> p, const Maps7 &tm, bool pairs, float *dlam,
     p.starts = reinterpret_cast<unsigned long long *>(ws + kWsHeader);
     Map *maps = reinterpret_cast<Map *>(ws + kWsHeader + up256(size_t(n) * size_t(segs) * 8));
     p.parts = reinterpret_cast<float *>(ws + carry_bytes(p.s.B, p.s.L, p.s.D));
-    if (p.pl.segs > 1 && !p.pl.local && cudaMemsetAsync(ws, 0, kWsHeader + size_t(n) * size_t(p.pl.segs) * 8, st) != cudaSuccess)
-        return SSM_ERR_CUDA;
+    if (!clear_words(p.pl, ws, n, st)) return SSM_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(p.pl.grid)), cfg.blockDim = dim3(unsigned(threads)), cfg.dynamicSmemBytes = smem, cfg.stream = st;
     cudaLaunchAttribute at;
@@ -1577,6 +1595,7 @@ ssm_status run_bwd(const ssm_gated_bwd_args *a, cudaStream_t st) {
     constexpr size_t es = sizeof(T);
     BwdArgs<T> p = {};
     p.s = {a->batch, a->seqlen, a->dim, ceil_div(a->dim, 64), a->c};
+    p.pl.drop_handoff = (a->flags & SSM_TEST_DROP_HANDOFF) != 0;
     p.counter = static_cast<unsigned int *>(a->workspace);
     p.x = static_cast<const T *>(a->x), p.r = static_cast<const T *>(a->r), p.i = static_cast<const T *>(a->i);
     p.dy = static_cast<const T *>(a->dy);
@@ -1621,7 +1640,7 @@ __global__ void gated_dlam_zero_kernel(int64_t D, float *dlam) {
 // What the forward and the backward check alike.
 template <typename A>
 ssm_status check_common(const A *a) {
-    if (!a || a->batch < 0 || a->seqlen < 0 || a->dim < 0 || a->flags != 0 || !(a->c > 0.0f) || a->c > FLT_MAX ||
+    if (!a || a->batch < 0 || a->seqlen < 0 || a->dim < 0 || (a->flags & ~uint32_t(SSM_TEST_DROP_HANDOFF)) || !(a->c > 0.0f) || a->c > FLT_MAX ||
         (a->dtype != SSM_F32 && a->dtype != SSM_BF16))
         return SSM_ERR_INVALID;
     if (!sizes_fit(a->batch, a->seqlen, a->dim, kChunk)) return SSM_ERR_UNSUPPORTED;
@@ -1768,6 +1787,18 @@ ssm_status ssm_gated_scan_bwd(const ssm_gated_bwd_args *args, void *stream) {
     if (!a->workspace || a->workspace_bytes < ssm_gated_scan_bwd_workspace_size(a)) return SSM_ERR_INVALID;
     if (!aligned(a->workspace, 16)) return SSM_ERR_UNSUPPORTED;
     return a->dtype == SSM_BF16 ? run_bwd<__nv_bfloat16>(a, st) : run_bwd<float>(a, st);
+}
+
+ssm_status ssm_gated_status(void *stream) {
+    static std::mutex one;  // gave_up_taken serves one query at a time
+    const std::lock_guard<std::mutex> hold(one);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    gave_up_take_kernel<<<1, 1, 0, st>>>();
+    unsigned int v = 0;
+    if (launched() != SSM_OK || cudaMemcpyFromSymbolAsync(&v, gave_up_taken, sizeof(v), 0, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return SSM_ERR_CUDA;
+    return static_cast<ssm_status>(v);
 }
 
 ssm_status ssm_gated_step(int64_t batch, int64_t dim, ssm_dtype dtype, float c, const void *x, int64_t x_stride,

@@ -148,3 +148,28 @@ def test_calls_keep_to_their_workspace(ssm, size, dtype):
     for k in want:
         assert torch.equal(want[k], got[k]), k
     assert ssm.workspace_status(ws) == 0 and (buf[back:] == 0xA5).all()
+
+
+def test_a_dropped_handoff_is_reported(ssm):
+    """A state that a segment does not hand on (a test hook of the library) makes its successor's bounded wait run out,
+    forward and backward: the workspace's status says so, and so does the device's where the scratch is gone; the calls
+    after it are right."""
+    from selective_state_space_47_b200 import _native
+    B, L, D = 1, 6000, 5120  # 80 columns of 47 tiles (94 in the backward): segments handed on in turn
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    n = lambda *s: torch.randn(*s, device="cuda", generator=gen)
+    x, r, i, dy = (n(B, L, D).to(BF16) for _ in range(4))
+    lam = torch.full((D,), -4.0, device="cuda")
+    drop, late = _native.SSM_TEST_DROP_HANDOFF, _native.SSM_ERR_TIMEOUT
+    y, st = ssm.gated_scan_fwd(x, r, i, lam, return_states=True)
+    want = ssm.gated_scan_bwd(x, r, i, lam, dy, states=st)
+    assert ssm.gated_status() == 0
+    ws = ssm.ScanWorkspace()
+    for call, right in ((lambda **k: ssm.gated_scan_fwd(x, r, i, lam, **k), y),
+                        (lambda **k: ssm.gated_scan_bwd(x, r, i, lam, dy, states=st, **k)["dx"], want["dx"])):
+        call(_test_flags=drop)
+        assert ssm.gated_status() == late and ssm.gated_status("cuda") == 0
+        call(_test_flags=drop, workspace=ws)
+        assert ssm.workspace_status(ws) == late and ssm.gated_status(stream=torch.cuda.current_stream()) == late
+        assert torch.equal(call(workspace=ws), right) and torch.equal(call(), right)
+        assert ssm.workspace_status(ws) == 0 and ssm.gated_status(0) == 0

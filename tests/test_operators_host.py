@@ -283,3 +283,15 @@ def test_nothing_is_kept_where_no_graph_is(monkeypatch, off):
             assert not call().requires_grad
     assert asked == [False] * 4
     assert all(call().requires_grad for call in calls) and asked[4:] == [True] * 4
+
+
+def test_test_hook_and_status_arguments(lib):
+    """The hand-off hook is a flag of the scan's calls, others are refused; the status is a CUDA device's."""
+    hook = _native.SSM_TEST_DROP_HANDOFF
+    assert lib.ssm_gated_scan_fwd(ctypes.byref(_gated(flags=hook, batch=0)), None) == OK
+    assert lib.ssm_gated_scan_bwd(ctypes.byref(_gated(True, flags=hook, dim=0)), None) == OK
+    for bad in (hook | 1, _native.SSM_SEQ_PARALLEL, _native.SSM_TEST_SHORT_SEGMENTS):
+        assert lib.ssm_gated_scan_fwd(ctypes.byref(_gated(flags=bad, batch=0)), None) == INVALID
+        assert lib.ssm_gated_scan_bwd(ctypes.byref(_gated(True, flags=bad, dim=0)), None) == INVALID
+    with pytest.raises(ValueError):
+        ssm.gated_status("cpu")
