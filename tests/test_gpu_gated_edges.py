@@ -5,7 +5,7 @@ import torch
 
 from tests import operators_ref as ref
 from tests.conftest import cuda_available
-from tests.test_gpu_gated import FWD, cuda, make
+from tests.test_gpu_gated import FWD, check_bwd, check_fwd, cuda, make
 
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
@@ -173,3 +173,51 @@ def test_a_dropped_handoff_is_reported(ssm):
         assert ssm.workspace_status(ws) == late and ssm.gated_status(stream=torch.cuda.current_stream()) == late
         assert torch.equal(call(workspace=ws), right) and torch.equal(call(), right)
         assert ssm.workspace_status(ws) == 0 and ssm.gated_status(0) == 0
+
+
+@pytest.mark.parametrize("extras", [False, True], ids=["plain", "h0_reset"])
+@pytest.mark.parametrize("B,L,D,dtype", [(4, 700, 517, F32), (8, 700, 330, F32), (8, 700, 330, BF16), (4, 700, 517, BF16), (5, 333, 320, BF16),
+                                         (5, 333, 320, F32), (30, 200, 66, F32), (30, 200, 66, BF16)])
+def test_every_loader_over_several_rounds(ssm, B, L, D, dtype, extras):
+    """More than 24 columns of several tiles each, by TMA, in pieces of two elements and one by one."""
+    d = make(B, L, D, dtype, seed=B * L + D, h0=extras, reset=0.01 if extras else 0.0, slow=not extras)
+    g = cuda(d)
+    _, (_, _, states) = check_fwd(ssm, d, g, dtype)
+    check_bwd(ssm, d, g, dtype, states)
+
+
+@pytest.mark.parametrize("B,L,D,dtype", [(1, 6000, 5120, BF16), (1, 5000, 2050, F32), (1, 9001, 1030, BF16), (1, 9001, 1031, BF16),
+                                         (2, 3000, 5120, F32), (1, 30000, 72, F32)])
+def test_dlam_over_segments_blocks_and_warps(ssm, B, L, D, dtype):
+    """dlam of chosen channels, a sum over everything that a plan cuts time and sequences into, against the formula over all
+    sequences."""
+    gen = torch.Generator(device="cuda").manual_seed(D - L)
+    n = lambda *s: torch.randn(*s, device="cuda", generator=gen)
+    g = {k: n(B, L, D).clamp(-6, 6).to(dtype) for k in ("x", "r", "i", "dy")}
+    g["lam"] = torch.log(torch.expm1(-torch.log(0.9 + 0.099 * torch.rand(D, device="cuda", generator=gen)) / 8.0))
+    g["h0"], g["dh_last"] = n(B, D), n(B, D)
+    reset = torch.rand(B, L, device="cuda", generator=gen) < 1e-3
+    got = ssm.gated_scan_bwd(*(g[k] for k in BWD), reset=reset)
+    sel = torch.tensor([0, 1, 63, 64, D // 2, D - 2, D - 1], device="cuda")
+    d = {k: v.index_select(v.dim() - 1, sel).cpu() for k, v in g.items()}
+    want, bound = ref.gated_scan_bwd(*(d[k] for k in BWD), reset=reset.cpu())
+    for k in want:
+        ref.check(got[k].index_select(got[k].dim() - 1, sel), want[k], bound[k], dtype if k in ("dx", "dr", "di") else F32, k)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,L,D", [(3, 150, 64), (2, 200, 33), (300, 9, 24), (40, 1, 64)], ids=lambda n: str(n))
+def test_tokens_laid_out_step_by_step(ssm, B, L, D, dtype):
+    """Tokens [L, B, D] in memory: the sequences lie closer together than the steps. In the step kernel too."""
+    d = make(B, L, D, dtype, seed=B + L + D, h0=True, reset=0.02)
+    g = cuda(d)
+    for k in "xri":
+        g[k] = g[k].transpose(0, 1).contiguous().transpose(0, 1)
+    _, (y, _, states) = check_fwd(ssm, d, g, dtype)
+    check_bwd(ssm, d, g, dtype, states)
+    h = g["h0"].clone()
+    d["reset"] = None
+    want, bound = ref.gated_scan(*(d[k][:, :1] if k in "xri" else d[k] for k in FWD))
+    out = ssm.gated_step(*(g[k][:, 0] for k in "xri"), g["lam"], h)
+    ref.check(out, want[:, 0], bound[:, 0], dtype, "y")
+    ref.check(h, want[:, 0], bound[:, 0], what="h")

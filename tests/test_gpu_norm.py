@@ -277,3 +277,52 @@ def test_a_recurrent_residual_layer(ssm):
                 assert (s + out - y[:, t]).abs().max() <= 2e-5 * want.abs().max()
     finally:
         torch.backends.cuda.matmul.allow_tf32 = old
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("dim", [64, 66, 4100, 4102])
+@pytest.mark.parametrize("residual", [False, True], ids=["alone", "residual"])
+def test_misaligned_arrays_backward(ssm, dtype, dim, residual):
+    """Arrays that start off 16 bytes, one at a time."""
+    d = make(9, dim, dtype, 13, residual)
+    g = cuda(d)
+    out = ssm.layer_norm_fwd(g["x"], g["weight"], g["bias"], g["residual"], return_stats=True)
+    mean, rstd = out[-2:]
+    t = dict(dy=g["dy"], s=out[1] if residual else g["x"], weight=g["weight"], dres=g["dres"])
+    want, bound = ref.layer_norm_bwd(d["dy"], t["s"].cpu(), d["weight"], mean.cpu(), rstd.cpu(), d["dres"])
+    for name in [k for k in t if t[k] is not None]:
+        h = dict(t)
+        buf = torch.empty(h[name].numel() + 1, dtype=h[name].dtype, device="cuda")
+        buf[1:] = h[name].reshape(-1)
+        h[name] = buf[1:].view(h[name].shape)
+        got = ssm.layer_norm_bwd(h["dy"], h["s"], h["weight"], mean, rstd, h["dres"], residual=residual)
+        for k in ("dx", "dweight", "dbias"):
+            ref.check(got[k], want[k], bound[k], dtype if k == "dx" else F32, f"{k}, {name} off its place")
+
+
+def test_streams_and_workspaces(ssm):
+    """Both directions on a stream of the caller's, and the backward with a workspace of exactly the bytes it asks for."""
+    import ctypes
+    from selective_state_space_47_b200 import _native
+    d = make(700, 264, BF16, 19, True)
+    g = cuda(d)
+    args = [g[k] for k in ("x", "weight", "bias", "residual")]
+    want = ssm.layer_norm_fwd(*args, return_stats=True)
+    grads = ssm.layer_norm_bwd(g["dy"], want[1], g["weight"], want[2], want[3], g["dres"], residual=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = ssm.layer_norm_fwd(*args, return_stats=True, stream=s)
+    gs = ssm.layer_norm_bwd(g["dy"], got[1], g["weight"], got[2], got[3], g["dres"], residual=True, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    a = _native.NormBwdArgs(700, 264, _native.SSM_BF16, 1)
+    need = _native.lib().ssm_layer_norm_bwd_workspace_size(ctypes.byref(a))
+    buf = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    gw = ssm.layer_norm_bwd(g["dy"], want[1], g["weight"], want[2], want[3], g["dres"], residual=True, workspace=buf[:need])
+    for k in grads:
+        assert torch.equal(grads[k], gs[k]) and torch.equal(grads[k], gw[k]), k
+    assert (buf[need:] == 0xA5).all()
+    for bad in (buf[:need - 1], torch.empty(need, dtype=torch.uint8)):
+        with pytest.raises(ValueError):
+            ssm.layer_norm_bwd(g["dy"], want[1], g["weight"], want[2], want[3], workspace=bad, residual=True)
