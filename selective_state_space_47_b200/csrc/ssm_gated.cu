@@ -327,7 +327,7 @@ struct Maps3 {
 
 constexpr int kFewColumns = 24;  // up to here LAG: 1536 channels of one sequence (575 against 496 us at L=131072)
 
-constexpr int kShort = 32, kShortBack = 16, kManyColumns = 256;  // up to so many tokens of at least so many columns: a thread per channel
+constexpr int kShortBack = 16;  // tokens that the few-token backward takes at most
 
 enum Load { kTma, kAsync, kPlain };  // 16-byte rows; pieces of 4 or 8 bytes; elements of 2 bytes
 
@@ -1230,8 +1230,8 @@ __global__ void __launch_bounds__(128)
 }
 
 // A few tokens of many sequences (a chunk of a decoding batch): a thread walks V neighbouring channels of one
-// sequence through all of them. Tiles would be mostly empty there (B=256 D=5120 bfloat16: 4 tokens 27 against 223 us, 32
-// tokens 104 against 231; from 64 on, 198 against 237, the tiles come level and then ahead: 128 tokens 387 against 260).
+// sequence through all of them, where tiles would be mostly empty (few_tokens_fwd says when). B=256 D=5120 bfloat16: 4 tokens 23 us,
+// 32 tokens 109 us, 2.0 and 4.9 TB/s; a thread's arithmetic is scalar, with two reciprocals and two exponentials an element.
 template <typename T, int V>
 __global__ void __launch_bounds__(128) gated_short_kernel(const FwdArgs<T> p) {
     const int64_t d = (int64_t(blockIdx.x) * 128 + threadIdx.x) * V;
@@ -1272,8 +1272,8 @@ __global__ void __launch_bounds__(128) gated_short_kernel(const FwdArgs<T> p) {
 }
 
 // Its backward: the states before the steps in registers, the tokens read a second time (from the caches) on the way back.
-// A thread's sums of dlam over its sequences are one value of the parts. (B=256 D=5120 bfloat16: 4 tokens 55 against 271 us,
-// 16 tokens 161 against 291; with an array for 32 tokens those cost 275, and 32 tokens 558 against 302.)
+// A thread's sums of dlam over its sequences are one value of the parts. B=256 D=5120 bfloat16: 4 tokens 59 us, 16 tokens 162 us,
+// both sweeps forming every gate. (With an array for 32 tokens those 16 cost 275, and 32 tokens 558 against 302 by tiles.)
 template <typename T, int V>
 __global__ void __launch_bounds__(128) gated_short_bwd_kernel(const BwdArgs<T> p) {
     const int64_t d = (int64_t(blockIdx.x) * 128 + threadIdx.x) * V;
@@ -1367,8 +1367,25 @@ size_t carry_bytes(int64_t B, int64_t L, int64_t D) {
     return kWsHeader + (segs > 1 ? 2 * up256(size_t(B) * size_t(D) * size_t(segs) * 8) : 0);
 }
 
-// Whether a call takes the few-token kernels: the forward up to kShort tokens, the backward up to kShortBack.
-bool few_tokens(int64_t B, int64_t L, int64_t D, int most) { return L <= most && B * ceil_div(D, 64) >= kManyColumns; }
+// Whether a call takes the few-token kernels, where a thread walks its channels through all tokens, rather than tiles, which
+// are then mostly empty. A thread's walk is a chain (0.9 us a token forward, 1.2 backward, beside 6 and 10 us) as long as the
+// GPU has room for all of them; the tiles' time goes by the columns (11 us for 64 bfloat16 ones forward, 22 for 1024, 221 for
+// 20480) and not by the tokens. So the border is a number of tokens that grows with the columns, up to where both are
+// bound by memory. Threads / tiles in us, in a graph: bfloat16 forward 16x16x1024 20/14, 32x8x1024 14/16, 64x16x1024 20/23,
+// 16x32x5120 35/25, 32x32x5120 37/40, 256x32x5120 109/228, 256x64x5120 199/238 but 256x64x1030 102/59; float32 forward 64x8x1024 16/16,
+// 64x32x1024 39/18, 64x24x5120 41/45, 256x32x5120 139/141. Rows below 256 channels leave lanes of a block idle: bfloat16
+// 4096x16x64 45/55, 4096x32x64 88/57, float32 4096x12x64 41/37, 4096x32x64 96/39.
+bool few_tokens_fwd(int64_t B, int64_t L, int64_t D, ssm_dtype dtype) {
+    const int64_t columns = B * ceil_div(D, 64);
+    if (dtype == SSM_BF16) return L <= std::min<int64_t>(D < 256 ? 24 : 32, 5 + columns / 92);
+    return L <= std::min<int64_t>(D < 256 ? 12 : 24, 4 + columns / 200);
+}
+// The same for the backward, either type: 32x6x1024 18/20, 32x16x1024 31/20, 64x12x1024 27/31, 256x16x5120 162/291; tiles of rows that TMA does
+// not take, or that are short, cost about twice as much a column: bfloat16 32x12x1001 22/30, 512x16x128 32/38, 1024x16x16 35/49.
+bool few_tokens_bwd(int64_t B, int64_t L, int64_t D, ssm_dtype dtype) {
+    const bool slow = D < 256 || D * (dtype == SSM_BF16 ? 2 : 4) % 16 != 0;
+    return L <= std::min<int64_t>(kShortBack, 2 + B * ceil_div(D, 64) / (slow ? 48 : 96));
+}
 int64_t short_rows(int64_t B) { return std::min<int64_t>(B, 2048); }  // of their backward's blocks, each a row of the parts
 
 // Clusters of each size that the GPU holds at once (0: not asked yet), by device.
@@ -1522,7 +1539,7 @@ ssm_status run_fwd(const ssm_gated_args *a, cudaStream_t st) {
     p.y = static_cast<T *>(a->y), p.h_last = a->h_last, p.states = a->states;
     const bool pairs = a->dim % 2 == 0 && even(a->x_stride) && even(a->r_stride) && even(a->i_stride) && aligned(a->x, 2 * es) &&
                        aligned(a->r, 2 * es) && aligned(a->i, 2 * es) && aligned(a->y, 2 * es);
-    if (few_tokens(a->batch, a->seqlen, a->dim, kShort)) {
+    if (few_tokens_fwd(a->batch, a->seqlen, a->dim, a->dtype)) {
         p.status = p.counter + 1;
         const bool four = (a->dim | p.xb | p.xt | p.rb | p.rt | p.ib | p.it) % 4 == 0 && aligned(a->x, 4 * es) && aligned(a->r, 4 * es) &&
                           aligned(a->i, 4 * es) && aligned(a->y, 4 * es);
@@ -1607,7 +1624,7 @@ ssm_status run_bwd(const ssm_gated_bwd_args *a, cudaStream_t st) {
     for (const void *q : {a->x, a->r, a->i, a->dy, static_cast<const void *>(a->dx), static_cast<const void *>(a->dr),
                           static_cast<const void *>(a->di)})
         pairs = pairs && aligned(q, 2 * es);
-    if (few_tokens(a->batch, a->seqlen, a->dim, kShortBack)) {
+    if (few_tokens_bwd(a->batch, a->seqlen, a->dim, a->dtype)) {
         p.status = p.counter + 1;
         p.parts = reinterpret_cast<float *>(static_cast<unsigned char *>(a->workspace) + kWsHeader);
         const dim3 grid(unsigned(ceil_div(a->dim, pairs ? 256 : 128)), unsigned(short_rows(a->batch)));
@@ -1706,7 +1723,7 @@ size_t ssm_gated_states_size(int64_t batch, int64_t seqlen, int64_t dim) {
 size_t ssm_gated_scan_workspace_size(const ssm_gated_args *a) {
     if (check_common(a) != SSM_OK) return 0;
     if (a->batch == 0 || a->dim == 0) return 0;
-    return few_tokens(a->batch, a->seqlen, a->dim, kShort) ? kWsHeader : carry_bytes(a->batch, a->seqlen, a->dim);
+    return few_tokens_fwd(a->batch, a->seqlen, a->dim, a->dtype) ? kWsHeader : carry_bytes(a->batch, a->seqlen, a->dim);
 }
 
 ssm_status ssm_gated_scan_fwd(const ssm_gated_args *args, void *stream) {
@@ -1744,7 +1761,7 @@ ssm_status ssm_gated_scan_fwd(const ssm_gated_args *args, void *stream) {
 size_t ssm_gated_scan_bwd_workspace_size(const ssm_gated_bwd_args *a) {
     if (check_common(a) != SSM_OK) return 0;
     if (a->batch == 0 || a->dim == 0) return 0;
-    if (few_tokens(a->batch, a->seqlen, a->dim, kShortBack)) return kWsHeader + size_t(short_rows(a->batch)) * size_t(a->dim) * 4;
+    if (few_tokens_bwd(a->batch, a->seqlen, a->dim, a->dtype)) return kWsHeader + size_t(short_rows(a->batch)) * size_t(a->dim) * 4;
     const int parts = most_parts(a->batch * ceil_div(a->dim, 64), ceil_div(a->seqlen, kChunk));
     return carry_bytes(a->batch, a->seqlen, a->dim) + size_t(a->batch) * size_t(a->dim) * size_t(parts) * kW * 4;
 }

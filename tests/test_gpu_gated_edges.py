@@ -21,8 +21,8 @@ def ssm():
     return m
 
 
-# whole tiles by TMA, rows in pieces, odd rows, two passes over few columns, a few tokens by threads
-FORMS = [(2, 400, 64), (2, 400, 34), (2, 400, 33), (1, 5000, 72), (300, 9, 12), (300, 9, 7)]
+# whole tiles by TMA, rows in pieces, odd rows, two passes over few columns, a few tokens by tiles and by threads
+FORMS = [(2, 400, 64), (2, 400, 34), (2, 400, 33), (1, 5000, 72), (300, 9, 12), (300, 9, 7), (1500, 9, 12), (1500, 9, 7)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
@@ -118,7 +118,8 @@ def test_a_workspace_is_held_on_another_stream(ssm, kind):
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("size", [(1, 1, 3), (2, 64, 70), (2, 65, 70), (3, 190, 64), (1, 700, 200), (1, 1100, 33), (4, 300, 2048), (40, 130, 600),
-                                  (1, 6000, 5120), (1, 50000, 72), (300, 3, 7), (2500, 16, 8), (300, 30, 64), (300, 64, 64)],
+                                  (1, 6000, 5120), (1, 50000, 72), (300, 3, 7), (2500, 16, 8), (300, 30, 64), (300, 64, 64), (40, 32, 5120),
+                                  (40, 16, 5120)],
                          ids=lambda s: "x".join(map(str, s)))
 def test_calls_keep_to_their_workspace(ssm, size, dtype):
     """With exactly the bytes asked for, and whatever they hold, results are as with scratch of the call's own, and what lies behind stays."""
@@ -221,3 +222,58 @@ def test_tokens_laid_out_step_by_step(ssm, B, L, D, dtype):
     out = ssm.gated_step(*(g[k][:, 0] for k in "xri"), g["lam"], h)
     ref.check(out, want[:, 0], bound[:, 0], dtype, "y")
     ref.check(h, want[:, 0], bound[:, 0], what="h")
+
+
+@pytest.mark.parametrize("extras", [False, True], ids=["plain", "h0_reset"])
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("B,L,D", [(3, 1, 200), (3, 2, 200), (3, 3, 200), (3, 4, 200), (3, 5, 200), (3, 6, 200), (3000, 9, 7), (2500, 16, 6), (2500, 20, 4),
+                                   (2500, 21, 4), (3000, 12, 5), (700, 16, 258), (700, 17, 257), (90, 32, 2050), (90, 33, 2048), (180, 24, 2049),
+                                   (180, 25, 2048)], ids=lambda n: str(n))
+def test_the_few_token_kernels_up_to_their_borders(ssm, B, L, D, dtype, extras):
+    """Sizes at both sides of the rules that choose between a thread a channel and tiles, in every width of a thread's piece."""
+    d = make(B, L, D, dtype, seed=B + L + D, h0=extras, reset=0.1 if extras else 0.0, slow=not extras)
+    g = cuda(d)
+    if extras:  # slices of one projection
+        both = torch.cat([g["r"], g["i"]], 2)
+        g["r"], g["i"] = both[:, :, :D], both[:, :, D:]
+    _, (_, _, states) = check_fwd(ssm, d, g, dtype)
+    got = check_bwd(ssm, d, g, dtype, states)
+    again = ssm.gated_scan_bwd(*(g[k] for k in BWD), reset=g["reset"])
+    for k in got:
+        assert torch.equal(got[k], again[k]), k
+
+
+def test_the_few_token_kernels_at_the_gates_ends(ssm):
+    """By threads, as by tiles: tiny rates keep their weight, a closed gate holds the state exactly with finite gradients, and a
+    reset keeps an infinity or NaN of what came before out of what follows."""
+    B, L, D = 1500, 9, 12
+    d = make(B, L, D, F32, seed=6, h0=True)
+    d["lam"] = torch.linspace(-60, -8, D)
+    g = cuda(d)
+    _, (_, _, states) = check_fwd(ssm, d, g, F32)
+    check_bwd(ssm, d, g, F32, states)
+    d["r"][:] = float("-inf")
+    g = cuda(d)
+    y, h, states = ssm.gated_scan_fwd(*(g[k] for k in FWD), return_last_state=True, return_states=True)
+    assert torch.equal(y, g["h0"][:, None].expand(-1, L, -1)) and torch.equal(h, g["h0"])
+    got = ssm.gated_scan_bwd(g["x"], g["r"], g["i"], g["lam"], g["dy"], None, g["dh_last"], states=states)
+    for k in ("dx", "dr", "di", "dlam"):
+        assert torch.equal(got[k], torch.zeros_like(got[k])), k
+    d = make(B, L, D, F32, seed=9, h0=True)
+    d["reset"] = torch.zeros(B, L, dtype=torch.bool)
+    d["reset"][:, 4] = True
+    bad = {k: None if v is None else v.clone() for k, v in d.items()}
+    bad["h0"][0] = float("inf")
+    bad["x"][1, 2] = NAN
+    bad["dy"][2, 6] = NAN
+    g = cuda(bad)
+    y, states = ssm.gated_scan_fwd(*(g[k] for k in FWD), reset=g["reset"], return_states=True)
+    want, bound = ref.gated_scan(*(d[k] for k in FWD), reset=d["reset"])
+    ref.check(y[:, 4:], want[:, 4:], bound[:, 4:], what="y after the reset")
+    ref.check(y[2:], want[2:], bound[2:], what="y")
+    got = ssm.gated_scan_bwd(g["x"], g["r"], g["i"], g["lam"], g["dy"], None, g["dh_last"], states=states, reset=g["reset"])
+    want, bound = ref.gated_scan_bwd(*(d[k] for k in BWD), reset=d["reset"])
+    for k in ("dx", "dr", "di"):
+        ref.check(got[k][:2, 4:], want[k][:2, 4:], bound[k][:2, 4:], what=k)
+        ref.check(got[k][2, :4], want[k][2, :4], bound[k][2, :4], what=k)
+        ref.check(got[k][3:], want[k][3:], bound[k][3:], what=k)

@@ -133,6 +133,18 @@ def test_gated_workspace_goes_by_the_length(lib, B, L, D, most):
     assert fore <= 1024 + (B * D * 16 * tiles if tiles > 1 else 0)
 
 
+@pytest.mark.parametrize("B,L,D,few", [(1, 2, 64, True), (1, 3, 64, False), (16, 4, 1024, True), (16, 8, 1024, False), (32, 7, 1024, True),
+                                       (32, 16, 1024, False), (64, 12, 1024, True), (64, 16, 1024, False), (128, 16, 1024, True), (300, 9, 12, False), (300, 8, 12, True),
+                                       (32, 12, 1001, True), (32, 16, 1001, False),
+                                       (2500, 16, 8, True), (256, 17, 5120, False), (256, 16, 5120, True)])
+def test_few_token_backward_is_chosen_where_it_is_faster(lib, B, L, D, few):
+    """By tokens and columns, as measured beside the rule; the scratch shows which form a call takes (4 bytes a channel of at
+    most 2048 rows, or 32 of each sequence's)."""
+    kw = dict(batch=B, seqlen=L, dim=D, x_stride=(L * D, D), r_stride=(L * D, D), i_stride=(L * D, D))
+    size = lib.ssm_gated_scan_bwd_workspace_size(ctypes.byref(_gated(True, **kw)))
+    assert size == 256 + (min(B, 2048) * D * 4 if few else B * D * 32)
+
+
 def test_gated_step_refuses(lib):
     def call(batch=2, dim=32, dtype=1, c=8.0, x=FAKE, xs=32, r=FAKE, rs=32, i=FAKE, i_s=32, lam=FAKE, h=FAKE,
              h_out=FAKE, y=FAKE + (1 << 16)):
