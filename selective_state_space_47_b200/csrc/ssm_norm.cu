@@ -513,7 +513,10 @@ ssm_status launch_bwd(NormBwd<T, S> p, int warps, float *dweight, float *dbias, 
     const int threads = ONE ? 32 * kOneWarpGroups : 32 * warps;
     const auto kernel = norm_bwd_kernel<T, S, VEC, CH, ONE>;
     const size_t smem = CH * VEC >= 32 ? size_t(p.dim) * 8 : 0;
-    const int blocks = resident_blocks(resident, reinterpret_cast<const void *>(kernel), warps, threads, smem ? 2 * kMaxDim * 4 : 0);
+    // asked with the longest row of so many warps, which is what `resident` is kept by (8192 x 4099 bfloat16, five warps
+    // a block: 427 us; with one block an SM, as the longest row of all would allow, 960)
+    const int longest = std::min(kMaxDim, warps * 32 * CH * VEC);
+    const int blocks = resident_blocks(resident, reinterpret_cast<const void *>(kernel), warps, threads, smem ? size_t(longest) * 8 : 0);
     if (blocks <= 0) return SSM_ERR_CUDA;
     // at least four rows to a group: fewer rows of partial sums where there is little to do
     p.groups = int(std::min<int64_t>(std::min(blocks * (ONE ? kOneWarpGroups : 1), p.groups), ceil_div(p.rows, 4)));

@@ -326,3 +326,21 @@ def test_streams_and_workspaces(ssm):
     for bad in (buf[:need - 1], torch.empty(need, dtype=torch.uint8)):
         with pytest.raises(ValueError):
             ssm.layer_norm_bwd(g["dy"], want[1], g["weight"], want[2], want[3], workspace=bad, residual=True)
+
+
+@pytest.mark.parametrize("dim,dtype", [(4099, BF16), (4098, BF16), (4099, F32)])
+def test_as_many_blocks_as_the_row_allows(ssm, dim, dtype):
+    """Where the backward's sums lie in shared memory, short rows leave room for several blocks on an SM, each with a row of
+    partial sums in the workspace; the gradients are right for any number of them."""
+    rows = 2400
+    d = make(rows, dim, dtype, 20, False)
+    g = cuda(d)
+    _, mean, rstd = ssm.layer_norm_fwd(g["x"], g["weight"], return_stats=True)
+    ws = torch.full((1 << 26,), 0xFF, dtype=torch.uint8, device="cuda")  # NaNs, where nothing is written
+    got = ssm.layer_norm_bwd(g["dy"], g["x"], g["weight"], mean, rstd, workspace=ws)
+    parts = ws[:600 * dim * 4].view(torch.float32).view(600, dim)
+    used = int((~torch.isnan(parts)).all(1).sum())
+    assert used > torch.cuda.get_device_properties(0).multi_processor_count
+    want, bound = ref.layer_norm_bwd(d["dy"], d["x"], d["weight"], mean.cpu(), rstd.cpu())
+    for k in want:
+        ref.check(got[k], want[k], bound[k], dtype if k == "dx" else F32, k)
