@@ -277,3 +277,60 @@ def test_the_few_token_kernels_at_the_gates_ends(ssm):
         ref.check(got[k][:2, 4:], want[k][:2, 4:], bound[k][:2, 4:], what=k)
         ref.check(got[k][2, :4], want[k][2, :4], bound[k][2, :4], what=k)
         ref.check(got[k][3:], want[k][3:], bound[k][3:], what=k)
+
+
+def test_two_calls_at_once(ssm):
+    """Calls that hand segments on in turn, on two streams that share the GPU, each forward and backward: the same bits as alone."""
+    B, L, D = 1, 6000, 5120
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    n = lambda *s: torch.randn(*s, device="cuda", generator=gen)
+    x, r, i, dy = (n(B, L, D).to(BF16) for _ in range(4))
+    lam = torch.full((D,), -4.0, device="cuda")
+    def both(a):
+        y, st = ssm.gated_scan_fwd(a, r, i, lam, return_states=True)
+        return (y, *ssm.gated_scan_bwd(a, r, i, lam, dy, states=st).values())
+    want = [both(a) for a in (x, dy)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(6):
+        for a, s in zip((x, dy), streams):
+            with torch.cuda.stream(s):
+                got.append(both(a))
+    torch.cuda.synchronize()
+    for k, res in enumerate(got):
+        for p, q in zip(res, want[k % 2]):
+            assert torch.equal(p, q)
+    assert ssm.gated_status() == 0
+
+
+def test_offsets_beyond_32_bits(ssm):
+    """2.2e9 elements a tensor: the last steps of the last sequence, forward from their kept state and backward from the end,
+    against the formulas; and the first steps of the first."""
+    B, L, D = 2, 215041, 5120
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.empty(B, L, D, device="cuda", dtype=BF16).normal_(generator=gen).clamp_(-6, 6)
+    lam = torch.log(torch.expm1(-torch.log(0.9 + 0.099 * torch.rand(D, device="cuda", generator=gen)) / 8.0))
+    y, h, states = ssm.gated_scan_fwd(x, x, x, lam, return_last_state=True, return_states=True)
+    sel = torch.tensor([0, 1, 2559, D - 1], device="cuda")
+    pick = lambda t: t.index_select(t.dim() - 1, sel).cpu()
+    t0 = L // 64 * 64 - 64  # a whole chunk and the last, short one
+    tail, l4 = pick(x[1:, t0:]), lam[sel].cpu()
+    want, bound = ref.gated_scan(tail, tail, tail, l4, pick(states[1:, t0 // 64]))
+    ref.check(pick(y[1:, t0:]), want, bound, BF16, "y")
+    ref.check(pick(h[1:]), want[:, -1], bound[:, -1], what="h_last")
+    head = pick(x[:1, :200])
+    want, bound = ref.gated_scan(head, head, head, l4)
+    ref.check(pick(y[:1, :200]), want, bound, BF16, "y")
+    del y
+    g = ssm.gated_scan_bwd(x, x, x, lam, x, states=states)
+    want, bound = ref.gated_scan_bwd(tail, tail, tail, l4, tail, pick(states[1:, t0 // 64]))
+    for k in ("dx", "dr", "di"):
+        ref.check(pick(g[k][1:, t0:]), want[k], bound[k], BF16, k)
+    assert all(torch.isfinite(g[k]).all() for k in ("dlam", "dh0"))
+    del g, states
+    # beyond 65535 sequences of a few tokens
+    d = make(70000, 2, 12, F32, seed=70, h0=True, reset=0.2)
+    c = cuda(d)
+    _, (_, _, states) = check_fwd(ssm, d, c, F32)
+    check_bwd(ssm, d, c, F32, states)

@@ -344,3 +344,19 @@ def test_as_many_blocks_as_the_row_allows(ssm, dim, dtype):
     want, bound = ref.layer_norm_bwd(d["dy"], d["x"], d["weight"], mean.cpu(), rstd.cpu())
     for k in want:
         ref.check(got[k], want[k], bound[k], dtype if k == "dx" else F32, k)
+
+
+def test_offsets_beyond_32_bits(ssm):
+    """2.2e9 elements: the last rows, both directions."""
+    rows, D = 1050001, 2112
+    x = torch.empty(rows, D, device="cuda", dtype=BF16).normal_()
+    w = 1 + 0.2 * torch.randn(D, device="cuda")
+    y, mean, rstd = ssm.layer_norm_fwd(x, w, return_stats=True)
+    tail = x[-5:].cpu()
+    want, bound = ref.layer_norm(tail, w.cpu())
+    ref.check(y[-5:], want["y"], bound["y"], BF16, "y")
+    ref.check(mean[-5:], want["mean"], bound["mean"], what="mean")
+    g = ssm.layer_norm_bwd(y, x, w, mean, rstd, bias=False)
+    want, bound = ref.layer_norm_bwd(y[-5:].cpu(), tail, w.cpu(), mean[-5:].cpu(), rstd[-5:].cpu())
+    ref.check(g["dx"][-5:], want["dx"], bound["dx"], BF16, "dx")
+    assert torch.isfinite(g["dweight"]).all()
