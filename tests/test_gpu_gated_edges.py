@@ -334,3 +334,35 @@ def test_offsets_beyond_32_bits(ssm):
     c = cuda(d)
     _, (_, _, states) = check_fwd(ssm, d, c, F32)
     check_bwd(ssm, d, c, F32, states)
+
+
+def test_a_training_step_captured(ssm):
+    """Norm, recurrence and their backward by autograd in one graph, replayed on new values, against the same step eager. No eager
+    graph of the captured leaves lives meanwhile (autograd would tie its stream into the capture)."""
+    B, L, D = 2, 300, 64
+    d = make(B, L, D, F32, seed=15, h0=True, reset=0.02)
+    g = cuda(d)
+    leaf = {k: g[k].clone().requires_grad_(True) for k in FWD}
+    w, b, s0 = (torch.ones(D, device="cuda").requires_grad_(True), torch.zeros(D, device="cuda").requires_grad_(True), torch.randn(B, L, D, device="cuda"))
+    inputs = [*leaf.values(), w, b]
+    def step():
+        z, s = ssm.layer_norm(leaf["x"], w, b, s0)
+        y, h = ssm.gated_scan(z, leaf["r"], leaf["i"], leaf["lam"], leaf["h0"], reset=g["reset"], return_last_state=True)
+        return [y.detach(), h.detach(), *torch.autograd.grad([y, h, s], inputs, [g["dy"], g["dh_last"], s0])]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for scale in (1.0, 0.7, 1.3):
+        with torch.no_grad():
+            for k in ("x", "r"):
+                leaf[k].copy_(g[k] * scale)
+        graph.replay()
+        torch.cuda.synchronize()
+        for p, q in zip(out, step()):
+            assert torch.equal(p, q)
