@@ -393,7 +393,7 @@ ssm_status ssm_ssd_fwd(const ssm_ssd_args *args, void *stream);
  *   w_t    = c softplus(lam[d]) sigmoid(r_t)
  *   a_t    = exp(-w_t),  beta_t = sqrt(1 - a_t^2)
  *   h_t    = a_t h_{t-1} + beta_t sigmoid(i_t) x_t,   y_t = h_t
- * and, where reset[b, t] is not 0 (a new document begins), a_t = 0 and beta_t = 1: the
+ * and, where reset[b, t] is not 0 (a new document begins), a_t = 0 and beta_t = 1, whatever r_t holds: the
  * state before it is dropped, whatever it holds. The state and every factor are float32
  * (1 - a_t is formed without cancellation); y is rounded once. Neighbouring pieces of
  * time are combined in an order that depends on the shape, the strides and the GPU alone,
@@ -405,7 +405,9 @@ ssm_status ssm_ssd_fwd(const ssm_ssd_args *args, void *stream);
  * + d (strides in elements, not negative; one over a single sequence or step does not count), so
  * that slices of one projection are read in place. All other arrays are contiguous. Any dim
  * and seqlen; tokens on their element size, float arrays on 4 bytes. Token rows on 16 bytes are
- * fetched by TMA, others in pieces of two elements or element by element (slower).
+ * fetched by TMA, others, and tokens whose sequences lie closer together than their steps, in pieces
+ * of two elements or element by element (slower). A workspace serves one call at a time: calls that may run at
+ * once, graphs captured with it among them, take one each.
  *
  * states (optional output) receives what the backward needs of the forward: the state
  * before every SSM_GATED_CHUNK-th step, [B, ceil(L / SSM_GATED_CHUNK), D] float32

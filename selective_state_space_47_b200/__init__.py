@@ -727,7 +727,8 @@ class _GatedScan(torch.autograd.Function):
 
 def gated_scan(x, r, i, lam, h0=None, *, reset=None, c=8.0, return_last_state=False):
     """The gated linear recurrence with its backward attached for torch.autograd: y (and the
-    final state) from gated_scan_fwd; gradients for x, r, i, lam and h0 from gated_scan_bwd."""
+    final state) from gated_scan_fwd; gradients for x, r, i, lam and h0 from gated_scan_bwd. (A training step captured into
+    a CUDA graph, as with any autograd function: let no eager graph of the same leaves live meanwhile.)"""
     if not torch.is_grad_enabled():  # (a Function's needs_input_grad goes by the tensors' own flags even then)
         return gated_scan_fwd(x, r, i, lam, h0, reset=reset, c=c, return_last_state=return_last_state)
     return _GatedScan.apply(x, r, i, lam, h0, reset, c, return_last_state)

@@ -12,11 +12,12 @@
 // passed over once, the state between rounds never leaves the chip, and the order in which pieces are
 // joined depends on the shape alone.
 //
-// What bounds it: the forward of B=1 L=262144 D=5120 bfloat16 takes 2.29 ms, 4.7 TB/s of 6.5, with the issue
-// slots at 53% and the special-function unit (four operations an element, 16 a clock) at 57%; with the
-// sigmoids and the root left out it takes 1.9 ms. The backward of B=8 L=4096 D=2048 takes 255 us, 3.7 TB/s, at 68
-// instructions an element on 51% of the issue slots. float32, with twice the bytes to the same arithmetic,
-// moves 6.3 TB/s forward and 5.2 TB/s backward there.
+// What bounds it: latency. The forward of B=1 L=262144 D=5120 bfloat16 takes 2.21 ms alone and 2.36 ms call after call, 4.9 and
+// 4.5 TB/s of 6.5; a computing warp waits once a tile for the way to the carrying warp, the cluster and back, and 16 such
+// warps an SM fill 53% of the issue slots and 57% of the special-function unit (four operations an element, 16 a clock)
+// meanwhile. With the sigmoids and the root left out it takes 1.9 ms. The backward of B=8 L=4096 D=2048 takes 254 us, 3.7
+// TB/s, at 68 instructions an element on 51% of the issue slots. float32, with twice the bytes to the same arithmetic, moves
+// 6.2 TB/s forward and 5.4 TB/s backward there.
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <float.h>
@@ -431,8 +432,9 @@ __device__ __forceinline__ void copy_async_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Loading warps. Three keep up with tiles that are fetched in small pieces; the backward in bfloat16 has one, for
-// the registers of its other warps (96 instead of 80: B=4 L=4096 D=2054 282 -> 205 us).
+// Loading warps. Three keep up with tiles that are fetched in small pieces; the backward in bfloat16 has one where rows come in
+// pairs, for the registers of its other warps (96 instead of 80: B=4 L=4096 D=2054 282 -> 205 us). Odd rows, which pass
+// through the loading warps' registers, keep three and 80, and spill most: 472 bytes stored and 784 loaded a thread.
 template <Load LOAD, bool BWD = false, int SIZE = 0>
 constexpr int kLoaders = LOAD == kTma || (LOAD == kAsync && BWD && SIZE == 2) ? 1 : 3;
 

@@ -6,9 +6,10 @@
 //
 // A row lives in the registers of a group of warps, CH vectors of VEC neighbouring columns in
 // each thread, from its one read to its one write; mean and variance take two passes over
-// those registers (the squares are of centred values, so a row far from zero loses
-// nothing). Bound by memory: 32768 x 2048 bfloat16 with a residual forward in 127 us (6.3 TB/s),
-// backward in 181 us (5.9 TB/s), without one 63 us (4.3 TB/s) and 90 us (4.5 TB/s).
+// those registers (the squares are of centred values, so a row far from zero keeps its variance).
+// Bound by memory: 32768 x 2048 bfloat16 with a residual forward in 127 us (6.3 TB/s), backward in 184 us (5.8
+// TB/s), float32 165 and 178 us (6.5 and 6.0 TB/s), without one 88 and 133 us (6.1 and 6.1 TB/s). bfloat16 without a residual
+// takes 66 us (4.1 TB/s) and 82 us (4.9 TB/s): two bytes a column, and only the rows in registers are on their way.
 #include <cuda_runtime.h>
 #include <float.h>
 #include <limits.h>
@@ -265,7 +266,9 @@ struct NormBwd {
 template <typename T, typename S, int VEC, int CH, bool ONE>
 __global__ void __launch_bounds__(32 * (ONE ? kOneWarpGroups : kMostWarps)) norm_bwd_kernel(const NormBwd<T, S> p) {
     constexpr bool KEEP = CH * VEC <= 16, SHARED = CH * VEC >= 32;
-    constexpr int SLOTS = 1;  // rows on their way (two of them spill registers: 121 against 104 us for 32768 x 2048 bfloat16)
+    // rows on their way: two take 121 against 104 us for 32768 x 2048 bfloat16, their registers spilled. (One spills as well, with
+    // 128 registers: 44 bytes stored and 56 loaded a thread in the form of this size with a residual, 16 and 12 without.)
+    constexpr int SLOTS = 1;
     __shared__ float buf[2][2][32];
     extern __shared__ __align__(16) float acc[];  // SHARED: [2][dim]
     const int threads = ONE ? 32 : blockDim.x, tid = ONE ? threadIdx.x & 31 : threadIdx.x;
