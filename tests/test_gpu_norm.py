@@ -360,3 +360,26 @@ def test_offsets_beyond_32_bits(ssm):
     want, bound = ref.layer_norm_bwd(y[-5:].cpu(), tail, w.cpu(), mean[-5:].cpu(), rstd[-5:].cpu())
     ref.check(g["dx"][-5:], want["dx"], bound["dx"], BF16, "dx")
     assert torch.isfinite(g["dweight"]).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_one_tensor_in_two_places(ssm, dtype):
+    """x as its own residual, and one tensor as token and both gates: gradients add up."""
+    d = make(7, 72, dtype, 21, False)
+    x, w = d["x"].cuda().requires_grad_(True), d["weight"].cuda().requires_grad_(True)
+    y, s = ssm.layer_norm(x, w, w, x if dtype is F32 else x.float())
+    gx, gw = torch.autograd.grad([y, s], [x, w], [d["dy"].cuda(), torch.ones_like(s)])
+    _, _, mean, rstd = ssm.layer_norm_fwd(x.detach(), w.detach(), w.detach(), x.detach().float(), return_stats=True)
+    want, bound = ref.layer_norm_bwd(d["dy"], s.detach().cpu(), d["weight"], mean.cpu(), rstd.cpu(), torch.ones(7, 72))
+    # bfloat16: each part and the sum are rounded, half a step of values of up to twice |dx| each
+    half = ref.HALF_STEP[dtype]
+    ref.check(gx, 2 * want["dx"], 2 * bound["dx"] + 3 * half * want["dx"].abs(), dtype, "dx")
+    ref.check(gw, want["dweight"] + want["dbias"], bound["dweight"] + bound["dbias"] + ref.U * (want["dweight"] + want["dbias"]).abs(), what="dweight")
+    n = torch.randn(2, 70, 8, generator=torch.Generator().manual_seed(1)).to(dtype)
+    t = n.cuda().requires_grad_(True)
+    lam = torch.full((8,), -3.0)
+    g, = torch.autograd.grad(ssm.gated_scan(t, t, t, lam.cuda()), t, n.cuda())
+    want, bound = ref.gated_scan_bwd(n, n, n, lam, n)
+    parts = [want[k] for k in ("dx", "dr", "di")]
+    mag = sum(p.abs() for p in parts)
+    ref.check(g, sum(parts), sum(bound[k] for k in ("dx", "dr", "di")) + 4 * half * mag, dtype, "d of all three")
